@@ -9,10 +9,11 @@ import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRCS = [os.path.join(PKG, "csrc", f) for f in ("fp_sparse.cu", "fp_prefill.cpp")]
+SRCS = [os.path.join(PKG, "csrc", f) for f in ("fp_sparse.cu", "fp_decode.cu", "fp_prefill.cpp")]
 DEPS = SRCS + [os.path.join(PKG, "csrc", f) for f in ("ptx.cuh", "index_kernels.cuh", "attn_kernel.cuh",
-                                                      "rope_pool.cuh", "share_kernels.cuh")] \
-    + [os.path.join(ROOT, "include", f) for f in ("fp_sparse.h", "fp_prefill.h")]
+                                                      "rope_pool.cuh", "share_kernels.cuh", "fp_internal.h",
+                                                      "rope_kernel.cuh", "kv_kernels.cuh", "tree_kernels.cuh")] \
+    + [os.path.join(ROOT, "include", f) for f in ("fp_sparse.h", "fp_prefill.h", "fp_decode.h")]
 LIB = os.path.join(PKG, "_lib", "libfpsparse.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 
@@ -24,7 +25,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     tmp = LIB + f".{os.getpid()}.tmp"
     cmd = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-           "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(ROOT, "include"), *SRCS, "-o", tmp]
+           "--threads", "4", "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(ROOT, "include"), *SRCS, "-o", tmp]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.check_call(cmd)

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "attn_kernel.cuh"
+#include "fp_internal.h"
 #include "fp_sparse.h"
 #include "index_kernels.cuh"
 #include "rope_pool.cuh"
@@ -175,6 +176,29 @@ bool make_map_split(CUtensorMap *m, const float *ptr, uint64_t rows) {
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+}  // namespace
+
+namespace fpk {
+
+int *library_error_word() { return device_error_word(); }
+
+bool make_byte_map(CUtensorMap *m, const void *ptr, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
+                   uint32_t box_rows) {
+  auto enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_bytes, box_rows};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace fpk
+
+namespace {
 
 uint64_t map_rows(int H, int ld, int S) { return (uint64_t)(H - 1) * (uint64_t)ld + (uint64_t)S; }
 
@@ -601,7 +625,8 @@ int fp_get_device_error(void *stream) {
   if (v != 0) {
     const int zero = 0;
     if (cudaMemcpy(err, &zero, 4, cudaMemcpyHostToDevice) != cudaSuccess) return FP_ERR_CUDA;
-    return (v & kDevErrTimeout) ? FP_ERR_TIMEOUT : FP_ERR_CUDA;
+    if (v & kDevErrTimeout) return FP_ERR_TIMEOUT;
+    return (v & kDevErrRange) ? FP_ERR_RANGE : FP_ERR_CUDA;
   }
   return FP_OK;
 }
@@ -819,6 +844,7 @@ const char *fp_strerror(int code) {
     case FP_ERR_CUDA: return "CUDA call failed";
     case FP_ERR_TIMEOUT: return "device wait timed out";
     case FP_ERR_STATE: return "index not built or built for another shape";
+    case FP_ERR_RANGE: return "an entry of a device table is out of range";
     default: return "unknown error";
   }
 }

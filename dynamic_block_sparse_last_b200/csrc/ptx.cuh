@@ -10,8 +10,9 @@
 
 namespace fpk {
 
-// Sticky device error bits (mirrored by FP_ERR_TIMEOUT on the host).
+// Sticky device error bits (mirrored by FP_ERR_TIMEOUT and FP_ERR_RANGE on the host).
 constexpr int kDevErrTimeout = 1;
+constexpr int kDevErrRange = 2;
 
 // A wait that has not completed after this long is treated as lost.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;

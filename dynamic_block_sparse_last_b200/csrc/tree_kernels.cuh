@@ -1,0 +1,850 @@
+// tree_kernels.cuh -- attention of drafted tokens over the paged cache, for
+// up to 32 query rows at a time (mma.sync), and the join of split sequences.
+//
+//   out_i = sum_p softmax_p(scale q_i . k_p) v_p
+// over the cached tokens p that new token i sees: all of the prefix, and the
+// new tokens that its mask names.
+//
+// Rows: the n new tokens of a sequence times the g query heads of one KV head
+// share that head's K and V, so a row tile is 16 * MT of those n g rows (row r:
+// token r / g, head r % g) and every K/V byte is read once per tile.
+//
+// Bound: memory.  A K/V byte serves 16 or 32 rows, 32-64 flops a byte over a
+// bf16 cache, well below what mma.sync sustains; so K and V stream through a
+// ring of TMA tiles (64 tokens each) and four warps take 16 tokens of a tile
+// each.  With 16 or 32 rows a tcgen05 tile (128 rows at least) would be mostly
+// padding, and its accumulators would have to come back through tensor memory.
+//
+// Work split: all (sequence, row tile, KV head) units, each of ceil(len / 64)
+// tiles, laid end to end, are cut into equal contiguous shares, one per CTA
+// (two CTAs per SM), whatever the lengths are; every CTA finds its share from
+// the lengths on the device, so nothing is planned on the host.  A unit inside
+// one share is finished there; the parts of the others go to the workspace (at
+// most two per CTA) and k_tree_join adds them up in a fixed order.
+//
+// Operand order: a matrix product does not mind the order of its inner index,
+// so K is taken in the order in which a thread's 16-byte shared-memory reads
+// bring it (Q's registers follow), and V's columns likewise: no ldmatrix, no
+// transposition through shared memory.  Quantised K and V are multiplied as
+// their codes, which fp16 holds exactly; K's scale goes to the scores and V's
+// to the probabilities, taken relative to a power of two near the largest seen
+// so far (kexp) so that they keep fp16's range.  bf16 queries over a quantised
+// cache are brought to fp16 by a power of two per row, exactly (elements below
+// 2^-14 of the row's largest lose bits from 2^-25 of it on).
+#pragma once
+
+#include <type_traits>
+
+#include "kv_kernels.cuh"
+#include "ptx.cuh"
+
+namespace fpk {
+
+constexpr int kTreeBN = 64;          // tokens of a tile
+constexpr int kTreeWarps = 4;        // consumer warps, 16 tokens of a tile each
+constexpr int kTreeThreads = (kTreeWarps + 1) * 32;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct TreeDesc {       // a unit split over several CTAs, written by the first of them
+  int seq_row0, n, j;   // first row of q / out, new tokens, KV head (n = 0: no such unit)
+  int row_tile0;        // first of its rows
+  int last;             // the CTA that holds its last tile
+  int pad[3];
+};
+
+struct TreeParams {
+  const float *scale[2];
+  const int *table, *kv_len, *cu;
+  const unsigned long long *mask;
+  const void *q;
+  void *out;
+  float *lse;
+  float *part;     // [2 C][BM][D]
+  float *part_ml;  // [2 C][BM][2]
+  TreeDesc *desc;  // [C]
+  int *err;
+  int64_t q_tok, q_head, o_tok, o_head, pages;
+  int max_pages, nseq, T, max_q, W, Hq, Hkv, g, page, page_shift, q_f16;
+  float scale2;    // scale * log2(e)
+};
+
+// A sequence's share of the work.
+struct TreeSeq {
+  int row0, n, len, nt, mt;
+};
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams &P, int s, int BM, int BN, bool report) {
+  TreeSeq q;
+  q.row0 = P.cu[s];
+  q.n = P.cu[s + 1] - q.row0;
+  q.len = P.kv_len[s];
+  q.nt = q.mt = 0;
+  if (q.n == 0) return q;
+  const bool ok = q.n > 0 && q.n <= P.max_q && q.row0 >= 0 && q.row0 <= P.T - q.n && q.len >= q.n &&
+                  (int64_t)q.len <= ((int64_t)P.max_pages << P.page_shift);
+  if (!ok) {
+    if (report) atomicOr(P.err, kDevErrRange);
+    q.n = 0;
+    return q;
+  }
+  q.nt = (q.len + BN - 1) / BN;
+  q.mt = (q.n * P.g + BM - 1) / BM;
+  return q;
+}
+
+struct TreeShare {
+  long long begin, end, chunk;   // tiles of this CTA; tiles per CTA
+  long long rem;                 // begin's place among the tiles of sequence s
+  int s;
+};
+
+// This CTA's share, found by all of its threads together.
+template <int NT>
+__device__ __forceinline__ void tree_share(const TreeParams &P, int BM, int BN, TreeShare *sh, long long *warp_sum) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (P.nseq + NT - 1) / NT;
+  const int s0 = min(tid * per, P.nseq), s1 = min(s0 + per, P.nseq);
+  long long own = 0;
+  for (int s = s0; s < s1; ++s) {
+    const TreeSeq q = tree_seq(P, s, BM, BN, blockIdx.x == 0);
+    own += (long long)q.nt * q.mt * P.Hkv;
+  }
+  long long inc = own;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  inc += before;
+  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+  const long long b = min((long long)blockIdx.x * chunk, total), e = min(b + chunk, total);
+  if (tid == 0) {
+    sh->begin = b;
+    sh->end = e;
+    sh->chunk = chunk;
+  }
+  long long at = inc - own;
+  if (b < e && b >= at && b < inc) {
+    for (int s = s0; s < s1; ++s) {
+      const TreeSeq q = tree_seq(P, s, BM, BN, false);
+      const long long c = (long long)q.nt * q.mt * P.Hkv;
+      if (b < at + c) {
+        sh->s = s;
+        sh->rem = b - at;
+        break;
+      }
+      at += c;
+    }
+  }
+  __syncthreads();
+}
+
+// The segments of a share: consecutive tiles of one unit.
+struct TreeWalk {
+  TreeSeq q;
+  int s, m, j, a, b;    // sequence, row tile, KV head, tiles [a, b) of the unit
+  long long left;       // tiles of the share from this segment on
+  __device__ __forceinline__ bool start(const TreeParams &P, const TreeShare &sh, int BM, int BN) {
+    left = sh.end - sh.begin;
+    if (left <= 0) return false;
+    s = sh.s;
+    q = tree_seq(P, s, BM, BN, false);
+    const long long u = sh.rem / q.nt;
+    a = (int)(sh.rem - u * q.nt);
+    m = (int)(u / P.Hkv);
+    j = (int)(u - (long long)m * P.Hkv);
+    b = (int)min((long long)q.nt, a + left);
+    return true;
+  }
+  __device__ __forceinline__ bool next(const TreeParams &P, int BM, int BN) {
+    left -= b - a;
+    if (left <= 0) return false;
+    if (++j == P.Hkv) {
+      j = 0;
+      if (++m == q.mt) {
+        m = 0;
+        do {
+          q = tree_seq(P, ++s, BM, BN, false);
+        } while (q.nt == 0);  // left > 0: another sequence has tiles
+      }
+    }
+    a = 0;
+    b = (int)min((long long)q.nt, left);
+    return true;
+  }
+};
+
+// Whether row token i of the sequence sees new token jj (0 <= jj < n).
+__device__ __forceinline__ bool tree_sees(const TreeParams &P, const TreeSeq &q, int i, int jj) {
+  if (!P.mask) return jj <= i;
+  return (P.mask[(int64_t)(q.row0 + i) * P.W + (jj >> 6)] >> (jj & 63)) & 1ull;
+}
+
+// One cached value of V as fp32 (the rare path of non-finite drafted values).
+template <int KIND, int D>
+__device__ __forceinline__ float tree_v_value(const TreeParams &P, const void *pool, int s, int j, int pos, int col) {
+  const int pg = P.table[(int64_t)s * P.max_pages + (pos >> P.page_shift)];
+  if (pg < 0 || pg >= P.pages) return 0.f;
+  const int64_t row = (((int64_t)pg * P.Hkv + j) << P.page_shift) + (pos & (P.page - 1));
+  if constexpr (KvCode<KIND>::kQuant) {
+    float x[4];
+    kv_values4<KIND>(static_cast<const uint8_t *>(pool)[row * D + col], x);
+    return x[0] * P.scale[1][row];
+  } else {
+    using C = typename std::conditional<KIND == kKvBf16, __nv_bfloat16, __half>::type;
+    return rope_to_float<C>(static_cast<const C *>(pool)[row * D + col]);
+  }
+}
+
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Four codes as two fp16 pairs.  int8 (with the sign bit flipped beforehand,
+// so b + 128): as the low byte of 1024 + u in fp16, minus 1152: exact.
+template <int KIND>
+__device__ __forceinline__ void tree_codes4(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if constexpr (KIND == kKvInt8) {
+    lo = hsub2(prmt(w, 0x64646464u, 0x4140u), 0x64806480u);
+    hi = hsub2(prmt(w, 0x64646464u, 0x4342u), 0x64806480u);
+  } else {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+template <int KIND>
+__device__ __forceinline__ void tree_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (KIND == kKvBf16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16 bytes of one cached V row with its non-finite values set to 0 (they are
+// added for the rows that see them at the end); *bad is raised when there were any.
+template <int KIND>
+__device__ __forceinline__ uint32_t tree_clean(uint32_t w, int &bad) {
+  if constexpr (KIND == kKvInt8) {
+    return w;
+  } else if constexpr (KIND == kKvE4m3) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (((w >> (8 * i)) & 0x7fu) == 0x7fu) {
+        w &= ~(0xffu << (8 * i));
+        bad = 1;
+      }
+    return w;
+  } else {
+    constexpr uint32_t E = KIND == kKvBf16 ? 0x7f80u : 0x7c00u;
+    if ((w & E) == E) {
+      w &= 0xffff0000u;
+      bad = 1;
+    }
+    if (((w >> 16) & E) == E) {
+      w &= 0xffffu;
+      bad = 1;
+    }
+    return w;
+  }
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+template <int KIND, int D, int MT>
+struct TreeCfg {
+  static constexpr bool kQuant = KvCode<KIND>::kQuant;
+  static constexpr int BM = 16 * MT;
+  static constexpr int RB = D * KvCode<KIND>::kBytes;     // bytes of a cached row
+  static constexpr int kBoxB = RB < 128 ? RB : 128;       // bytes of a box row
+  static constexpr int kBoxes = RB / kBoxB;
+  static constexpr int E = 16 / KvCode<KIND>::kBytes;     // elements of 16 bytes
+  static constexpr int kSteps = D / 16;
+  static constexpr int VE = (kQuant && D == 128) ? 16 : 8;  // V columns of a thread's read
+  static constexpr int kTile = kTreeBN * RB;              // K (or V) bytes of a tile
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = kStage >= 32768 ? (MT == 1 ? 3 : 2) : (kStage >= 16384 ? 5 : 8);
+  static constexpr int kScaleOff = kStages * kStage;      // [stage][K, V][64] fp32
+  static constexpr int kQOff = kScaleOff + (kQuant ? kStages * 2 * kTreeBN * 4 : 0);  // [MT][steps][32] uint4
+  static constexpr int kLd = D + 4;                       // row pitch of obuf (fp32)
+  static constexpr int kOOff = kQOff + MT * kSteps * 512;
+  static constexpr int kSmem = kOOff + BM * kLd * 4 + 1024;
+};
+
+// Shared address of the 16-byte chunk `ch` of row r of a tile (TMA swizzle:
+// 128-byte rows by row mod 8, 64-byte rows by row / 2 mod 4; 256-byte rows are
+// two boxes of 128).
+template <typename C>
+__device__ __forceinline__ uint32_t tree_chunk(uint32_t tile, int r, int ch) {
+  if constexpr (C::kBoxB == 128)
+    return tile + (ch >> 3) * (kTreeBN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+  else
+    return tile + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+}
+
+template <int KIND, int D, int MT>
+__global__ void __launch_bounds__(kTreeThreads, 2)
+    k_tree(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+           const __grid_constant__ TreeParams P, const void *v_pool) {
+  using C = TreeCfg<KIND, D, MT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
+  __shared__ long long warp_sum[kTreeThreads / 32];
+  __shared__ TreeShare share;
+  __shared__ float red_m[kTreeWarps][C::BM], red_l[kTreeWarps][C::BM], row_scale[C::BM], fin_m[C::BM], fin_l[C::BM];
+  __shared__ int abort_sh, bad_sh;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  if (threadIdx.x == 0) {
+    abort_sh = 0;
+    bad_sh = 0;
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(smem_u32(&bar_full[i]), 1);
+      mbar_init(smem_u32(&bar_empty[i]), kTreeWarps);
+    }
+    fence_mbar_init();
+  }
+  tree_share<kTreeThreads>(P, C::BM, kTreeBN, &share, warp_sum);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  volatile int *abort_flag = &abort_sh;
+  TreeWalk w;
+  bool more = w.start(P, share, C::BM, kTreeBN);
+
+  if (warp == kTreeWarps) {
+    // ------------------------------------------------------------ producer
+    // A tile is 64 / min(page, 64) pieces, each of one page; lane i moves piece i.
+    const int piece = min(P.page, kTreeBN), pieces = kTreeBN / piece;
+    if (lane == 0) {
+      tma_prefetch_map(&tm_k);
+      tma_prefetch_map(&tm_v);
+    }
+    int u = 0;
+    bool ok = true;
+    for (; more && ok; more = w.next(P, C::BM, kTreeBN)) {
+      const int *tab = P.table + (int64_t)w.s * P.max_pages;
+      int pg = 0;
+      const int p0 = w.a * kTreeBN + lane * piece;
+      if (lane < pieces && p0 < w.q.len) pg = tab[p0 >> P.page_shift];
+      for (int t = w.a; t < w.b; ++t, ++u) {
+        const int pos = t * kTreeBN + lane * piece;
+        const bool mine = lane < pieces && pos < w.q.len;
+        const int now = pg;
+        const int nx = pos + kTreeBN;  // the next tile's page, ahead of its use
+        if (t + 1 < w.b && lane < pieces && nx < w.q.len) pg = tab[nx >> P.page_shift];
+        const int st = u % C::kStages;
+        if (u >= C::kStages) ok = mbar_wait(smem_u32(&bar_empty[st]), ((u / C::kStages) - 1) & 1, abort_flag, P.err);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        const int n = __popc(__ballot_sync(0xffffffffu, mine));
+        const uint32_t bar = smem_u32(&bar_full[st]);
+        if (lane == 0) mbar_expect_tx(bar, n * piece * (2 * C::RB + (C::kQuant ? 8 : 0)));
+        __syncwarp();
+        if (mine) {
+          int id = now;
+          if (id < 0 || id >= P.pages) {
+            id = 0;
+            atomicOr(P.err, kDevErrRange);
+          }
+          const int row = ((id * P.Hkv + w.j) << P.page_shift) + (pos & (P.page - 1));
+          const uint32_t dst = base + st * C::kStage + lane * piece * C::kBoxB;
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x) {
+            tma_load_2d(dst + x * kTreeBN * 128, &tm_k, x * 128, row, bar);
+            tma_load_2d(dst + C::kTile + x * kTreeBN * 128, &tm_v, x * 128, row, bar);
+          }
+          if constexpr (C::kQuant) {
+            const uint32_t sd = base + C::kScaleOff + st * 2 * kTreeBN * 4 + lane * piece * 4;
+            bulk_load(sd, P.scale[0] + row, piece * 4, bar);
+            bulk_load(sd + kTreeBN * 4, P.scale[1] + row, piece * 4, bar);
+          }
+        }
+      }
+    }
+    // a CTA may not end with copies in flight: the consumers wait for every
+    // tile; after an abandoned wait nothing reads them, so wait here
+    if (!ok)
+      for (int i = 0; i < C::kStages; ++i)
+        if (u - 1 - i >= 0) {
+          const int v = u - 1 - i;
+          const unsigned long long t0 = globaltimer();
+          while (!mbar_try_wait(smem_u32(&bar_full[v % C::kStages]), (v / C::kStages) & 1) &&
+                 globaltimer() - t0 < kWaitLimitNs) {
+          }
+        }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int q4 = lane >> 2, c4 = lane & 3;
+  const uint32_t qbase = base + C::kQOff;
+  float *obuf = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)) + C::kOOff);
+  constexpr int NC = kTreeWarps * 32;
+  int u = 0;
+  if (threadIdx.x == 0) P.desc[blockIdx.x].n = 0;
+  long long at = share.begin;  // tile index of the segment's first tile
+  for (; more; at += w.b - w.a, more = w.next(P, C::BM, kTreeBN)) {
+    const int prefix = w.q.len - w.q.n, rbase = w.m * C::BM, R = min(C::BM, w.q.n * P.g - rbase);
+    // Q fragments: a warp takes a row, a lane 4 neighbouring elements, which are
+    // one thread's (a0, a2) or (a1, a3) of one step
+    for (int r = warp; r < C::BM; r += kTreeWarps) {
+      uint32_t lo = 0, hi = 0;
+      float fac = 1.f;
+      if (r < R && lane < D / 4) {
+        const int i = (rbase + r) / P.g, h = w.j * P.g + (rbase + r) % P.g;
+        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(P.q) +
+                                                         (w.q.row0 + i) * P.q_tok + h * P.q_head + 4 * lane);
+        lo = x.x;
+        hi = x.y;
+      }
+      if (C::kQuant && !P.q_f16) {
+        float x[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
+                      __uint_as_float(hi & 0xffff0000u)};
+        float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+        mx = redux_max_f32(mx);
+        int e = (int)(__float_as_uint(mx) >> 23) - 127;  // largest in [2^e, 2^(e+1))
+        e = e > 126 ? 0 : (e < -126 ? -126 : e);
+        fac = pow2i(e);
+        const float inv = pow2i(-e);
+        lo = pack_f16x2(x[0] * inv, x[1] * inv);
+        hi = pack_f16x2(x[2] * inv, x[3] * inv);
+      }
+      if (lane < D / 4) {
+        const int chunk = 4 * lane / C::E, jj = (4 * lane % C::E) / 4, step = (chunk >> 2) * (C::E / 4) + jj;
+        const int dl = (r & 7) * 4 + (chunk & 3);
+        const uint32_t dst = qbase + (((r >> 4) * C::kSteps + step) * 32 + dl) * 16 + ((r >> 3) & 1) * 4;
+        asm volatile("st.shared.b32 [%0], %1;\n\tst.shared.b32 [%0+8], %2;" ::"r"(dst), "r"(lo), "r"(hi) : "memory");
+      }
+      if (lane == 0) row_scale[r] = fac * P.scale2;
+    }
+    named_sync(1, NC);
+    uint32_t qf[MT == 1 ? C::kSteps : 1][4];
+    if constexpr (MT == 1) {
+#pragma unroll
+      for (int k = 0; k < C::kSteps; ++k) {
+        const uint4 x = lds128(qbase + (k * 32 + lane) * 16);
+        qf[k][0] = x.x; qf[k][1] = x.y; qf[k][2] = x.z; qf[k][3] = x.w;
+      }
+    }
+    float rs[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      rs[mt][0] = row_scale[16 * mt + q4];
+      rs[mt][1] = row_scale[16 * mt + 8 + q4];
+    }
+    float o[MT][D / 8][4];
+    float m[MT][2], l[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][i][e] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+    int kexp = -126;
+    int bad = 0;
+    for (int t = w.a; t < w.b; ++t, ++u) {
+      const int st = u % C::kStages;
+      // after an abandoned wait the warps still walk to the end together (the
+      // barriers below have no time limit of their own); the results are lost
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_full[st]), (u / C::kStages) & 1, abort_flag, P.err))) break;
+      const uint32_t kt = base + st * C::kStage, vt = kt + C::kTile;
+      const int key0 = warp * 16;
+      const int pos0 = t * kTreeBN + key0;
+      const bool tail = pos0 + 16 > prefix;
+      // ---- scores of 16 tokens
+      float s[MT][2][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
+#pragma unroll
+      for (int h = 0; h < C::RB / 64; ++h) {
+        uint32_t kw[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 x = lds128(tree_chunk<C>(kt, key0 + 8 * i + q4, c4 + 4 * h));
+          kw[i][0] = x.x; kw[i][1] = x.y; kw[i][2] = x.z; kw[i][3] = x.w;
+        }
+#pragma unroll
+        for (int jj = 0; jj < C::E / 4; ++jj) {
+          const int step = h * (C::E / 4) + jj;
+          uint32_t b[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (C::kQuant) {
+              tree_codes4<KIND>(KIND == kKvInt8 ? kw[i][jj] ^ 0x80808080u : kw[i][jj], b[i][0], b[i][1]);
+            } else {
+              b[i][0] = kw[i][2 * jj];
+              b[i][1] = kw[i][2 * jj + 1];
+            }
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint32_t a[4];
+            if constexpr (MT == 1) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) a[e] = qf[step][e];
+            } else {
+              const uint4 x = lds128(qbase + ((mt * C::kSteps + step) * 32 + lane) * 16);
+              a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
+            }
+            tree_mma<KIND>(s[mt][0], a, b[0][0], b[0][1]);
+            tree_mma<KIND>(s[mt][1], a, b[1][0], b[1][1]);
+          }
+        }
+      }
+      // ---- scales and masks
+      float vs[4] = {1.f, 1.f, 1.f, 1.f};  // V scales of tokens 2c, 2c+1, 8+2c, 9+2c
+      if constexpr (C::kQuant) {
+        const uint32_t sc = base + C::kScaleOff + st * 2 * kTreeBN * 4 + (key0 + 2 * c4) * 4;
+        const uint2 k0 = lds64(sc), k1 = lds64(sc + 32);
+        const uint2 v0 = lds64(sc + kTreeBN * 4), v1 = lds64(sc + kTreeBN * 4 + 32);
+        const float ks[4] = {__uint_as_float(k0.x), __uint_as_float(k0.y), __uint_as_float(k1.x), __uint_as_float(k1.y)};
+        vs[0] = __uint_as_float(v0.x); vs[1] = __uint_as_float(v0.y);
+        vs[2] = __uint_as_float(v1.x); vs[3] = __uint_as_float(v1.y);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][i][e] *= ks[2 * i + (e & 1)] * rs[mt][e >> 1];
+      } else {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][i][e] *= rs[mt][e >> 1];
+      }
+      uint32_t hide = 0;  // bit (mt * 8 + i * 4 + e): not visible
+      if (tail) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const int i = min((rbase + 16 * mt + 8 * hh + q4) / P.g, w.q.n - 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int pos = pos0 + 8 * (e >> 1) + 2 * c4 + (e & 1);
+              const bool vis = pos < prefix || (pos < w.q.len && tree_sees(P, w.q, i, pos - prefix));
+              if (!vis) {
+                s[mt][e >> 1][2 * hh + (e & 1)] = -INFINITY;
+                hide |= 1u << (mt * 8 + (e >> 1) * 4 + 2 * hh + (e & 1));
+              }
+            }
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (pos0 + 8 * (e >> 1) + 2 * c4 + (e & 1) >= w.q.len) vs[e] = 0.f;
+      }
+      // ---- softmax with the running maximum of this warp's tokens
+      float kfac = 1.f;
+      bool moved = false;
+      if constexpr (C::kQuant) {
+        float mx = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = mx < INFINITY ? min((int)(__float_as_uint(mx) >> 23) - 127, 126) : -127;  // NaN scales do not count
+        if (e > kexp + 4) {  // uniform in the warp; probabilities times scales stay below 2^5
+          kfac = e - kexp > 126 ? 0.f : pow2i(kexp - e);
+          kexp = e;
+          moved = true;
+        }
+        const float kinv = pow2i(-kexp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vs[i] *= kinv;
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        float al[2];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float mx = fmaxf(fmaxf(s[mt][0][2 * hh], s[mt][0][2 * hh + 1]), fmaxf(s[mt][1][2 * hh], s[mt][1][2 * hh + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const float mn = fmaxf(m[mt][hh], mx);
+          al[hh] = mn > m[mt][hh] ? ex2(m[mt][hh] - mn) : 1.f;
+          moved |= mn > m[mt][hh];
+          m[mt][hh] = mn;
+          const float ref = mn == -INFINITY ? 0.f : mn;
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = ex2(s[mt][e >> 1][2 * hh + (e & 1)] - ref);
+          l[mt][hh] = l[mt][hh] * al[hh] + ((p[0] + p[1]) + (p[2] + p[3]));
+          if constexpr (C::kQuant) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              p[e] *= vs[e];
+              if (tail && (hide >> (mt * 8 + (e >> 1) * 4 + 2 * hh + (e & 1))) & 1u) p[e] = 0.f;
+            }
+          }
+          pa[mt][hh] = KIND == kKvBf16 ? pack_bf16x2(p[0], p[1]) : pack_f16x2(p[0], p[1]);
+          pa[mt][2 + hh] = KIND == kKvBf16 ? pack_bf16x2(p[2], p[3]) : pack_f16x2(p[2], p[3]);
+        }
+        al[0] *= kfac;
+        al[1] *= kfac;
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][i][e] *= al[e >> 1];
+        }
+      }
+      // ---- O += P V
+#pragma unroll
+      for (int x = 0; x < C::kBoxes; ++x) {
+        uint32_t vw[4][C::VE * KvCode<KIND>::kBytes / 4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = key0 + 8 * (e >> 1) + 2 * c4 + (e & 1);
+          if constexpr (C::VE * KvCode<KIND>::kBytes == 16) {
+            const uint4 y = lds128(tree_chunk<C>(vt, r, q4 + 8 * x));
+            vw[e][0] = y.x; vw[e][1] = y.y; vw[e][2] = y.z; vw[e][3] = y.w;
+          } else {
+            const uint2 y = lds64(tree_chunk<C>(vt, r, q4 >> 1) + (q4 & 1) * 8);
+            vw[e][0] = y.x; vw[e][1] = y.y;
+          }
+        }
+        if (tail) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int pos = pos0 + 8 * (e >> 1) + 2 * c4 + (e & 1);
+#pragma unroll
+            for (int k = 0; k < C::VE * KvCode<KIND>::kBytes / 4; ++k) {
+              if (pos >= w.q.len) vw[e][k] = 0u;
+              else if (pos >= prefix) vw[e][k] = tree_clean<KIND>(vw[e][k], bad);
+            }
+          }
+        }
+        if constexpr (C::kQuant) {
+#pragma unroll
+          for (int k = 0; k < C::VE / 4; ++k) {
+            uint32_t b0[4], b1[4];  // columns 4k .. 4k+3
+            const uint32_t fl = KIND == kKvInt8 ? 0x80808080u : 0u;
+            tree_codes4<KIND>(prmt(vw[0][k], vw[1][k], 0x5140u) ^ fl, b0[0], b0[1]);
+            tree_codes4<KIND>(prmt(vw[0][k], vw[1][k], 0x7362u) ^ fl, b0[2], b0[3]);
+            tree_codes4<KIND>(prmt(vw[2][k], vw[3][k], 0x5140u) ^ fl, b1[0], b1[1]);
+            tree_codes4<KIND>(prmt(vw[2][k], vw[3][k], 0x7362u) ^ fl, b1[2], b1[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) tree_mma<KIND>(o[mt][4 * k + i], pa[mt], b0[i], b1[i]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t sel = i ? 0x7632u : 0x5410u;
+              const uint32_t b0 = prmt(vw[0][k], vw[1][k], sel), b1 = prmt(vw[2][k], vw[3][k], sel);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) tree_mma<KIND>(o[mt][8 * x + 2 * k + i], pa[mt], b0, b1);
+            }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
+    }
+    // ---- join the four warps
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        l[mt][hh] += __shfl_xor_sync(0xffffffffu, l[mt][hh], 1);
+        l[mt][hh] += __shfl_xor_sync(0xffffffffu, l[mt][hh], 2);
+        if (c4 == 0) {
+          red_m[warp][16 * mt + 8 * hh + q4] = m[mt][hh];
+          red_l[warp][16 * mt + 8 * hh + q4] = l[mt][hh];
+        }
+      }
+    if (bad) bad_sh = 1;
+    named_sync(1, NC);
+    float f[MT][2];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = 16 * mt + 8 * hh + q4;
+        float M = red_m[0][r];
+#pragma unroll
+        for (int k = 1; k < kTreeWarps; ++k) M = fmaxf(M, red_m[k][r]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+#pragma unroll
+        for (int k = 0; k < kTreeWarps; ++k) L += red_l[k][r] * ex2(red_m[k][r] - ref);
+        f[mt][hh] = ex2(m[mt][hh] - ref) * (C::kQuant ? pow2i(kexp) : 1.f);
+        if (warp == 0 && c4 == 0) {
+          fin_m[r] = M;
+          fin_l[r] = L;
+        }
+      }
+    for (int k = 0; k < kTreeWarps; ++k) {
+      if (warp == k) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            float *row = obuf + (16 * mt + 8 * hh + q4) * C::kLd;
+#pragma unroll
+            for (int x = 0; x < C::kBoxes; ++x)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < C::VE; i += 4) {
+                  float4 *dst = reinterpret_cast<float4 *>(row + 64 * x + C::VE * (2 * c4 + e) + i);
+                  float4 v = k == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *dst;
+                  const int oi = C::VE * x + i, oe = 2 * hh + e;
+                  v.x = fmaf(o[mt][oi][oe], f[mt][hh], v.x);
+                  v.y = fmaf(o[mt][oi + 1][oe], f[mt][hh], v.y);
+                  v.z = fmaf(o[mt][oi + 2][oe], f[mt][hh], v.z);
+                  v.w = fmaf(o[mt][oi + 3][oe], f[mt][hh], v.w);
+                  *dst = v;
+                }
+          }
+      }
+      named_sync(1, NC);
+    }
+    // ---- out, or this CTA's part of it
+    const bool whole = w.a == 0 && w.b == w.q.nt;
+    const int slot = 2 * blockIdx.x + (w.a == 0 ? 1 : 0);
+    const int fixup = bad_sh;
+    for (int x = threadIdx.x; x < R * (D / 4); x += NC) {
+      const int r = x / (D / 4), col = 4 * (x % (D / 4));
+      const int i = (rbase + r) / P.g, h = w.j * P.g + (rbase + r) % P.g;
+      float4 v = *reinterpret_cast<const float4 *>(obuf + r * C::kLd + col);
+      const float L = fin_l[r];
+      if (whole) {
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
+      }
+      if (fixup) {
+        float *vv = reinterpret_cast<float *>(&v);
+        for (int jj = 0; jj < w.q.n; ++jj) {
+          const int pos = prefix + jj;
+          if (pos < w.a * kTreeBN || pos >= w.b * kTreeBN || !tree_sees(P, w.q, i, jj)) continue;
+          for (int e = 0; e < 4; ++e) {
+            const float y = tree_v_value<KIND, D>(P, v_pool, w.s, w.j, pos, col + e);
+            if (!(fabsf(y) < INFINITY)) vv[e] += y;
+          }
+        }
+      }
+      if (whole) {
+        uint2 y;
+        if (P.q_f16) y = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
+        else y = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + (w.q.row0 + i) * P.o_tok + h * P.o_head + col) = y;
+        if (col == 0 && P.lse) P.lse[(int64_t)h * P.T + w.q.row0 + i] = L == 0.f ? -INFINITY : (fin_m[r] + __log2f(L)) * kLn2;
+      } else {
+        *reinterpret_cast<float4 *>(P.part + ((int64_t)slot * C::BM + r) * D + col) = v;
+        if (col == 0) {
+          P.part_ml[((int64_t)slot * C::BM + r) * 2] = fin_m[r];
+          P.part_ml[((int64_t)slot * C::BM + r) * 2 + 1] = L;
+        }
+      }
+    }
+    if (w.a == 0 && !whole && threadIdx.x == 0) {
+      TreeDesc d = {};
+      d.seq_row0 = w.q.row0;
+      d.n = w.q.n;
+      d.j = w.j;
+      d.row_tile0 = rbase;
+      d.last = (int)((at + w.q.nt - 1) / share.chunk);
+      P.desc[blockIdx.x] = d;
+    }
+    named_sync(1, NC);  // obuf and the Q fragments are free again
+    if (threadIdx.x == 0) bad_sh = 0;
+  }
+}
+
+// Adds up the parts of the units that several CTAs share, in the order of the
+// CTAs.  grid (C, row groups of 8), a thread per 4 columns.
+template <int D>
+__global__ void __launch_bounds__(8 * D / 4) k_tree_join(const __grid_constant__ TreeParams P, int BM) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const TreeDesc d = P.desc[blockIdx.x];
+  if (d.n == 0) return;
+  const int R = min(BM, d.n * P.g - d.row_tile0);
+  const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
+  if (r >= R) return;
+  const int c0 = blockIdx.x;
+  float M = -INFINITY;
+  for (int c = c0; c <= d.last; ++c) {
+    const int slot = 2 * c + (c == c0 ? 1 : 0);
+    M = fmaxf(M, P.part_ml[((int64_t)slot * BM + r) * 2]);
+  }
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= d.last; ++c) {
+    const int64_t at = (int64_t)(2 * c + (c == c0 ? 1 : 0)) * BM + r;
+    const float2 ml = *reinterpret_cast<const float2 *>(P.part_ml + at * 2);
+    const float4 v = *reinterpret_cast<const float4 *>(P.part + at * D + col);
+    const float f = ex2(ml.x - ref);
+    L = fmaf(ml.y, f, L);
+    acc.x = fmaf(v.x, f, acc.x);
+    acc.y = fmaf(v.y, f, acc.y);
+    acc.z = fmaf(v.z, f, acc.z);
+    acc.w = fmaf(v.w, f, acc.w);
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  const int i = (d.row_tile0 + r) / P.g, h = d.j * P.g + (d.row_tile0 + r) % P.g;
+  uint2 y;
+  if (P.q_f16) y = make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
+  else y = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + (d.seq_row0 + i) * P.o_tok + h * P.o_head + col) = y;
+  if (col == 0 && P.lse) P.lse[(int64_t)h * P.T + d.seq_row0 + i] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+}
+
+}  // namespace fpk

@@ -1,4 +1,4 @@
-"""Python binding of the C ABI in include/fp_sparse.h (ctypes).
+"""Python binding of the C ABI in include/*.h (ctypes).
 
 Argument marshalling only: torch tensors are passed as device pointers and
 the current CUDA stream as a handle; every step of the computation runs in
@@ -14,9 +14,12 @@ import torch
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "libfpsparse.so")
 
-FP_OK, FP_ERR_ARG, FP_ERR_CUDA, FP_ERR_TIMEOUT, FP_ERR_STATE = 0, 1, 2, 3, 4
+FP_OK, FP_ERR_ARG, FP_ERR_CUDA, FP_ERR_TIMEOUT, FP_ERR_STATE, FP_ERR_RANGE = 0, 1, 2, 3, 4, 5
 FP_QK_BF16, FP_QK_INT8 = 0, 1
 FP_PATTERN_VS, FP_PATTERN_QA = 0, 1
+FP_DT_BF16, FP_DT_F16, FP_DT_F32, FP_DT_INT8, FP_DT_E4M3 = 0, 1, 2, 3, 4
+FP_ROPE_HALF, FP_ROPE_INTERLEAVED = 0, 1
+FP_ROPE_NONE, FP_ROPE_LINEAR, FP_ROPE_BASE, FP_ROPE_BANDS, FP_ROPE_RAMP = 0, 1, 2, 3, 4
 
 SYMBOLS = ("fp_index_create", "fp_index_free", "fp_build_index", "fp_sparse_attn", "fp_index_info",
            "fp_index_nnz", "fp_index_export", "fp_get_device_error", "fp_debug_wait_timeout",
@@ -25,7 +28,9 @@ SYMBOLS = ("fp_index_create", "fp_index_free", "fp_build_index", "fp_sparse_attn
            "fp_index_group_lists",
            "fp_prefill_create", "fp_prefill_free", "fp_prefill_enqueue", "fp_prefill_wait", "fp_prefill_run",
            "fp_prefill_group_index", "fp_varlen_create", "fp_varlen_free", "fp_varlen_build_index",
-           "fp_varlen_sparse_attn", "fp_varlen_index", "fp_rope_pool", "fp_build_index_pooled")
+           "fp_varlen_sparse_attn", "fp_varlen_index", "fp_rope_pool", "fp_build_index_pooled",
+           "fp_rope_create", "fp_rope_free", "fp_rope_freqs", "fp_rope_apply",
+           "fp_kv_create", "fp_kv_free", "fp_kv_write", "fp_kv_read", "fp_tree_attn_workspace", "fp_tree_attn")
 
 
 class FpError(RuntimeError):
@@ -75,8 +80,22 @@ def _load():
     L.fp_varlen_build_index.argtypes = [vp, vp, vp, f, f, i, vp, vp, vp]
     L.fp_varlen_sparse_attn.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp]
     L.fp_varlen_index.argtypes = [vp, i, ctypes.POINTER(vp)]
+    n, dbl, sz = ctypes.c_int64, ctypes.c_double, ctypes.c_size_t
+    L.fp_rope_create.argtypes = [i, i, i, dbl, i, dbl, dbl, dbl, dbl, dbl, ctypes.POINTER(vp)]
+    L.fp_rope_freqs.argtypes = [vp, vp]
+    L.fp_rope_apply.argtypes = [vp] + [vp, n, n] * 4 + [i, i, i, i, vp, i, vp]
+    L.fp_kv_create.argtypes = [vp, vp, vp, vp, i, n, i, i, i, ctypes.POINTER(vp)]
+    L.fp_kv_write.argtypes = [vp] + [vp, n, n] * 2 + [i, i, vp, vp]
+    L.fp_kv_read.argtypes = [vp, vp, i, vp, vp, i, i] + [vp, n, n] * 2 + [i, vp]
+    L.fp_tree_attn_workspace.argtypes = [i] * 5
+    L.fp_tree_attn_workspace.restype = sz
+    L.fp_tree_attn.argtypes = [vp, vp, n, n, i, i, i, vp, i, vp, vp, i, i, vp, f, vp, n, n, vp, vp, sz, vp]
+    for name in ("fp_rope_free", "fp_kv_free"):
+        getattr(L, name).argtypes = [vp]
+        getattr(L, name).restype = None
     for s in SYMBOLS:
-        if s not in ("fp_index_free", "fp_strerror", "fp_prefill_free", "fp_varlen_free"):
+        if s not in ("fp_index_free", "fp_strerror", "fp_prefill_free", "fp_varlen_free", "fp_rope_free", "fp_kv_free",
+                     "fp_tree_attn_workspace"):
             getattr(L, s).restype = i
     return L
 
@@ -353,3 +372,203 @@ class Varlen:
             self.free()
         except Exception:
             pass
+
+
+# ---------------------------------------------------------------- fp_decode.h
+# Tensors of tokens are torch tensors [heads, tokens, d] with any strides whose
+# last one is 1 (head-major tensors, or transposed views of token-major rows).
+
+_DTYPES = {torch.bfloat16: FP_DT_BF16, torch.float16: FP_DT_F16, torch.float32: FP_DT_F32, torch.int8: FP_DT_INT8,
+           torch.float8_e4m3fn: FP_DT_E4M3}
+
+
+def _refuse(where, why):
+    raise FpError(FP_ERR_ARG, f"{where}: {why}")
+
+
+def _on(where, device, *tensors):
+    """Every tensor is on `device`, and that is the current device: its stream is the one used."""
+    if device.type != "cuda":
+        _refuse(where, "tensors must be on a CUDA device")
+    for t in tensors:
+        if t is not None and t.device != device:
+            _refuse(where, f"tensors on {t.device} and {device}")
+    if torch.cuda.current_device() != device.index:
+        _refuse(where, f"tensors on {device}, which is not the current device")
+
+
+def _table(where, name, t, dtype, *shape):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _tokens(where, name, t, dtype, *shape):
+    if t.dtype != dtype or t.shape != shape or t.stride(2) != 1:
+        _refuse(where, f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous elements")
+
+
+def _rows(t):
+    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(1), t.stride(0))
+
+
+class Rope:
+    """The rotary frequencies of one model (fp_rope; host memory only).  The
+    first rot_dim (default: all) of d elements of a head are rotated; scaling
+    is one of FP_ROPE_*, with its parameters as include/fp_decode.h says."""
+
+    def __init__(self, d, rot_dim=None, layout=FP_ROPE_HALF, theta=10000.0, scaling=FP_ROPE_NONE, factor=1.0,
+                 orig_len=0.0, low=0.0, high=0.0, amplitude=1.0):
+        self.handle = None
+        self.d, self.rot_dim, self.layout = d, d if rot_dim is None else rot_dim, layout
+        h = ctypes.c_void_p()
+        _check(_lib.fp_rope_create(d, self.rot_dim, layout, theta, scaling, factor, orig_len, low, high, amplitude,
+                                   ctypes.byref(h)), "fp_rope_create")
+        self.handle = h.value
+
+    def freqs(self):
+        """Radians per position of the rot_dim/2 pairs, fp64."""
+        import numpy as np
+        f = np.zeros(self.rot_dim // 2)
+        _check(_lib.fp_rope_freqs(self.handle, f.ctypes.data), "fp_rope_freqs")
+        return f
+
+    def apply(self, q_in, k_in, q_out, k_out, pos, inverse=False, stream=None):
+        """Rotates q_in [Hq, T, d] and k_in [Hkv, T, d] (either may be None, with its
+        output) by the positions pos (int32 [T]) into q_out, k_out (which may be the
+        inputs); inverse: the transpose, the gradient of the inputs."""
+        where, any_in = "fp_rope_apply", q_in if q_in is not None else k_in
+        if any_in is None:
+            _refuse(where, "neither q nor k")
+        T, d = any_in.shape[1:] if any_in.dim() == 3 else (0, 0)
+        _on(where, any_in.device, q_in, k_in, q_out, k_out, pos)
+        for name, x, y in (("q", q_in, q_out), ("k", k_in, k_out)):
+            if (x is None) != (y is None):
+                _refuse(where, f"{name}_in and {name}_out go together")
+            if x is not None:
+                _tokens(where, name + "_in", x, any_in.dtype, x.shape[0], T, self.d)
+                _tokens(where, name + "_out", y, any_in.dtype, x.shape[0], T, self.d)
+        _table(where, "pos", pos, torch.int32, T)
+        _check(_lib.fp_rope_apply(self.handle, *_rows(q_in), *_rows(k_in), *_rows(q_out), *_rows(k_out),
+                                  _DTYPES.get(any_in.dtype, -1), T, 0 if q_in is None else q_in.shape[0],
+                                  0 if k_in is None else k_in.shape[0], pos.data_ptr(), int(inverse), _stream(stream)),
+               where)
+
+    def free(self):
+        if self.handle:
+            _lib.fp_rope_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+class KvCache:
+    """A paged key/value cache over caller-owned pools (fp_kv): k_pool, v_pool
+    [pages, Hkv, page, d] bf16, fp16, int8 or float8_e4m3fn, and for the latter two
+    k_scale, v_scale fp32 [pages, Hkv, page].  The pools are kept alive."""
+
+    def __init__(self, k_pool, v_pool, k_scale=None, v_scale=None):
+        self.handle = None
+        where = "fp_kv_create"
+        if k_pool.dim() != 4:
+            _refuse(where, "pools are [pages, Hkv, page, d]")
+        pages, self.Hkv, self.page, self.d = k_pool.shape
+        _on(where, k_pool.device, k_pool, v_pool, k_scale, v_scale)
+        for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+            _table(where, name, t, k_pool.dtype, *k_pool.shape)
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None:
+                _table(where, name, t, torch.float32, *k_pool.shape[:3])
+        self.pools, self.pages, self.device = (k_pool, v_pool, k_scale, v_scale), pages, k_pool.device
+        h = ctypes.c_void_p()
+        _check(_lib.fp_kv_create(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+                                 _DTYPES.get(k_pool.dtype, -1), pages, self.page, self.Hkv, self.d, ctypes.byref(h)), where)
+        self.handle = h.value
+
+    def write(self, k, v, slots, stream=None):
+        """Writes the tokens k, v [Hkv, T, d] (either may be None) to slots (int64 [T],
+        page * page_size + offset; negative: skipped), quantising each row."""
+        where, x = "fp_kv_write", k if k is not None else v
+        if x is None:
+            _refuse(where, "neither k nor v")
+        _on(where, self.device, k, v, slots)
+        T = x.shape[1] if x.dim() == 3 else 0
+        for name, t in (("k", k), ("v", v)):
+            if t is not None:
+                _tokens(where, name, t, x.dtype, self.Hkv, T, self.d)
+        _table(where, "slots", slots, torch.int64, T)
+        _check(_lib.fp_kv_write(self.handle, *_rows(k), *_rows(v), _DTYPES.get(x.dtype, -1), T, slots.data_ptr(),
+                                _stream(stream)), where)
+
+    def read(self, block_table, cu_seqlens, k, v, first=None, stream=None):
+        """Reads cached tokens into k, v [Hkv, T, d] (either may be None): rows
+        cu_seqlens[s] .. cu_seqlens[s+1]-1 receive the tokens first[s] (default 0), ..
+        of sequence s.  block_table int32 [nseq, max_pages], cu_seqlens int32
+        [nseq + 1], first int32 [nseq], on the device."""
+        where, x = "fp_kv_read", k if k is not None else v
+        if x is None:
+            _refuse(where, "neither k nor v")
+        _on(where, self.device, k, v, block_table, cu_seqlens, first)
+        T = x.shape[1] if x.dim() == 3 else 0
+        for name, t in (("k", k), ("v", v)):
+            if t is not None:
+                _tokens(where, name, t, x.dtype, self.Hkv, T, self.d)
+        if block_table.dim() != 2:
+            _refuse(where, "block_table is [nseq, max_pages]")
+        nseq, width = block_table.shape
+        _table(where, "block_table", block_table, torch.int32, nseq, width)
+        _table(where, "cu_seqlens", cu_seqlens, torch.int32, nseq + 1)
+        if first is not None:
+            _table(where, "first", first, torch.int32, nseq)
+        _check(_lib.fp_kv_read(self.handle, block_table.data_ptr(), width, cu_seqlens.data_ptr(), _ptr(first), nseq, T,
+                               *_rows(k), *_rows(v), _DTYPES.get(x.dtype, -1), _stream(stream)), where)
+
+    def free(self):
+        if self.handle:
+            _lib.fp_kv_free(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def fp_tree_attn_workspace(nseq, max_q, Hq, Hkv, d) -> int:
+    """Bytes of workspace of fp_tree_attn on the current device."""
+    n = _lib.fp_tree_attn_workspace(nseq, max_q, Hq, Hkv, d)
+    if n == 0:
+        _refuse("fp_tree_attn_workspace", "sizes out of range, or no usable device")
+    return n
+
+
+def fp_tree_attn(q, kv: KvCache, block_table, kv_len, cu_q, max_q, mask, scale, out, work, lse=None, stream=None):
+    """Attention of the new tokens q [Hq, T, d] (rows cu_q[s] .. of sequence s, at
+    most max_q each) over the kv_len[s] cached tokens of their sequences, the last
+    of which are the new ones; mask int64 [T, ceil(max_q/64)] (bit j of row i: token
+    i sees new token j of its sequence) or None for j <= i.  Into out [Hq, T, d] and
+    lse fp32 [Hq, T]; work: a uint8 tensor of fp_tree_attn_workspace bytes."""
+    where = "fp_tree_attn"
+    if q.dim() != 3 or block_table.dim() != 2:
+        _refuse(where, "q is [Hq, T, d], block_table [nseq, max_pages]")
+    Hq, T, d = q.shape
+    nseq, width = block_table.shape
+    _on(where, kv.device, q, block_table, kv_len, cu_q, mask, out, work, lse)
+    _tokens(where, "q", q, q.dtype, Hq, T, kv.d)
+    _tokens(where, "out", out, q.dtype, Hq, T, kv.d)
+    _table(where, "block_table", block_table, torch.int32, nseq, width)
+    _table(where, "kv_len", kv_len, torch.int32, nseq)
+    _table(where, "cu_q", cu_q, torch.int32, nseq + 1)
+    if mask is not None:
+        _table(where, "mask", mask, torch.int64, T, (max_q + 63) // 64)
+    if lse is not None:
+        _table(where, "lse", lse, torch.float32, Hq, T)
+    if not work.is_contiguous():
+        _refuse(where, "work must be contiguous")
+    _check(_lib.fp_tree_attn(kv.handle, *_rows(q), _DTYPES.get(q.dtype, -1), T, Hq, block_table.data_ptr(), width,
+                             kv_len.data_ptr(), cu_q.data_ptr(), nseq, max_q, _ptr(mask), scale, *_rows(out), _ptr(lse),
+                             work.data_ptr(), work.numel() * work.element_size(), _stream(stream)), where)

@@ -54,7 +54,8 @@ enum {
     FP_ERR_ARG = 1,      /* invalid argument (shape, pointer, alignment, range) */
     FP_ERR_CUDA = 2,     /* a CUDA runtime/driver call failed (launch, copy, alloc) */
     FP_ERR_TIMEOUT = 3,  /* a device-side bounded wait gave up */
-    FP_ERR_STATE = 4     /* index used before it was built, or built for other shapes */
+    FP_ERR_STATE = 4,    /* index used before it was built, or built for other shapes */
+    FP_ERR_RANGE = 5     /* a kernel met an entry out of range in a device table (fp_decode.h) */
 };
 
 enum { FP_QK_BF16 = 0, FP_QK_INT8 = 1 };        /* element type of q and k */
@@ -176,7 +177,8 @@ int fp_index_classes(const fp_index *idx, int32_t *cls, void *stream);
 int fp_choose_block_size(const fp_index *idx, float gamma, int *b, float *rho, void *stream);
 
 /* Synchronises `stream`, returns FP_OK or the sticky device error recorded by
- * a kernel on the current device (FP_ERR_TIMEOUT), and clears it. */
+ * a kernel on the current device (FP_ERR_TIMEOUT, else FP_ERR_RANGE), and
+ * clears it. */
 int fp_get_device_error(void *stream);
 
 /* Test hook for the bounded-wait path: launches one CTA that waits on a
