@@ -10,6 +10,7 @@
 #include "kv_kernels.cuh"
 #include "rope_kernel.cuh"
 #include "tree_kernels.cuh"
+#include "tree_tc.cuh"
 
 using namespace fpk;
 
@@ -371,8 +372,11 @@ bool tree_shape_ok(int nseq, int max_q, int Hq, int Hkv, int d) {
          (d == 64 || d == 128);
 }
 
-// Rows of a tile for at most `rows` query rows of a KV head.
-int tree_bm(int rows) { return rows <= 16 ? 16 : 32; }
+// Query rows of a unit for at most `rows` rows of a KV head, the tokens of a
+// tile and the CTAs that go with it.
+int tree_bm(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
+int tree_bn(int bm) { return bm <= 32 ? kTreeBN : kTcBN; }
+int tree_ctas(int bm) { return bm <= 32 ? 2 * sms() : sms(); }
 
 struct TreeWork {
   size_t part, ml, desc, bytes;
@@ -394,15 +398,12 @@ bool allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
 }
 
-template <int KIND, int D, int MT>
-int launch_tree(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st) {
-  using C = TreeCfg<KIND, D, MT>;
-  if (!allow_smem(k_tree<KIND, D, MT>, C::kSmem)) return FP_ERR_CUDA;
-  k_tree<KIND, D, MT><<<ctas, kTreeThreads, C::kSmem, st>>>(kv->map[0], kv->map[1], P, kv->g.pool[1]);
-  int rc = status();
-  if (rc) return rc;
+// The parts of split units are added up by a launch of its own, which may be
+// set up while the first one still runs.
+template <int D>
+int launch_join(const TreeParams &P, int bm, int ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (C::BM + 7) / 8);
+  cfg.gridDim = dim3(ctas, (bm + 7) / 8);
   cfg.blockDim = dim3(8 * D / 4);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
@@ -410,13 +411,39 @@ int launch_tree(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st)
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_tree_join<D>, P, (int)C::BM) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_tree_join<D>, P, bm) == cudaSuccess ? FP_OK : FP_ERR_CUDA;
 }
 
+template <int KIND, int D, int MT>
+int launch_tree(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st) {
+  using C = TreeCfg<KIND, D, MT>;
+  if (!allow_smem(k_tree<KIND, D, MT>, C::kSmem)) return FP_ERR_CUDA;
+  k_tree<KIND, D, MT><<<ctas, kTreeThreads, C::kSmem, st>>>(kv->map[0], kv->map[1], P, kv->g.pool[1]);
+  const int rc = status();
+  return rc ? rc : launch_join<D>(P, C::BM, ctas, st);
+}
+
+template <int KIND, int D, bool PAIR>
+int launch_tree_tc(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st) {
+  using C = TcCfg<KIND, D, PAIR>;
+  if (!allow_smem(k_tree_tc<KIND, D, PAIR>, C::kSmem)) return FP_ERR_CUDA;
+  k_tree_tc<KIND, D, PAIR><<<ctas, kTcThreads, C::kSmem, st>>>(kv->map[0], kv->map[1], P, kv->g.pool[1]);
+  const int rc = status();
+  return rc ? rc : launch_join<D>(P, C::BM, ctas, st);
+}
+
+template <int KIND, int D>
+int launch_tree_kind(const fp_kv *kv, const TreeParams &P, int bm, int ctas, cudaStream_t st) {
+  switch (bm) {
+    case 16: return launch_tree<KIND, D, 1>(kv, P, ctas, st);
+    case 32: return launch_tree<KIND, D, 2>(kv, P, ctas, st);
+    case 128: return launch_tree_tc<KIND, D, false>(kv, P, ctas, st);
+    default: return launch_tree_tc<KIND, D, true>(kv, P, ctas, st);
+  }
+}
 template <int KIND>
 int launch_tree_kind(const fp_kv *kv, const TreeParams &P, int bm, int ctas, cudaStream_t st) {
-  if (kv->d == 128) return bm == 16 ? launch_tree<KIND, 128, 1>(kv, P, ctas, st) : launch_tree<KIND, 128, 2>(kv, P, ctas, st);
-  return bm == 16 ? launch_tree<KIND, 64, 1>(kv, P, ctas, st) : launch_tree<KIND, 64, 2>(kv, P, ctas, st);
+  return kv->d == 128 ? launch_tree_kind<KIND, 128>(kv, P, bm, ctas, st) : launch_tree_kind<KIND, 64>(kv, P, bm, ctas, st);
 }
 
 }  // namespace
@@ -425,9 +452,9 @@ extern "C" {
 
 size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d) {
   if (!tree_shape_ok(nseq, max_q, Hq, Hkv, d)) return 0;
-  const int n = sms();
-  if (!n) return 0;
-  return tree_work(2 * n, tree_bm(max_q * (Hq / Hkv)), d).bytes;
+  if (!sms()) return 0;
+  const int bm = tree_bm(max_q * (Hq / Hkv));
+  return tree_work(tree_ctas(bm), bm, d).bytes;
 }
 
 int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, int dtype, int T, int Hq,
@@ -437,7 +464,7 @@ int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, 
   if (!kv || T < 0 || max_pages < 0 || !tree_shape_ok(nseq, max_q, Hq, kv->g.heads, kv->d)) return FP_ERR_ARG;
   if (dtype != FP_DT_BF16 && dtype != FP_DT_F16) return FP_ERR_ARG;
   if ((kv->dtype == FP_DT_BF16 || kv->dtype == FP_DT_F16) && kv->dtype != dtype) return FP_ERR_ARG;
-  if (!std::isfinite(scale)) return FP_ERR_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FP_ERR_ARG;
   if (T == 0 || nseq == 0) return FP_OK;
   if (!rows_ok(q, q_tok, q_head, 2) || !rows_ok(out, o_tok, o_head, 2)) return FP_ERR_ARG;
   if (!block_table || !kv_len || !cu_q || !multiple_of(block_table, 4) || !multiple_of(kv_len, 4) ||
@@ -445,15 +472,15 @@ int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, 
     return FP_ERR_ARG;
   if (!work || !multiple_of(work, 16)) return FP_ERR_ARG;
   if (!on_device(kv)) return FP_ERR_ARG;
-  const int n = sms();
-  if (!n) return FP_ERR_CUDA;
+  if (!sms()) return FP_ERR_CUDA;
   const int g = Hq / kv->g.heads, bm = tree_bm(max_q * g);
-  const TreeWork w = tree_work(2 * n, bm, kv->d);
+  const int most = tree_ctas(bm);
+  const TreeWork w = tree_work(most, bm, kv->d);
   if (work_bytes < w.bytes) return FP_ERR_ARG;
   // no more CTAs than there can be tiles
   const double tiles = (double)nseq * ((max_q * g + bm - 1) / bm) * kv->g.heads *
-                       std::ceil((double)max_pages * kv->g.page / kTreeBN);
-  const int ctas = tiles < 2 * n ? (tiles < 1 ? 1 : (int)tiles) : 2 * n;
+                       std::ceil((double)max_pages * kv->g.page / tree_bn(bm));
+  const int ctas = tiles < most ? (tiles < 1 ? 1 : (int)tiles) : most;
   TreeParams P;
   P.scale[0] = kv->g.scale[0];
   P.scale[1] = kv->g.scale[1];

@@ -149,9 +149,9 @@ __device__ __forceinline__ void tree_share(const TreeParams &P, int BM, int BN, 
 struct TreeWalk {
   TreeSeq q;
   int s, m, j, a, b;    // sequence, row tile, KV head, tiles [a, b) of the unit
-  long long left;       // tiles of the share from this segment on
+  int left;             // tiles of the share from this segment on (a share is below 2^31: a sequence's tokens are)
   __device__ __forceinline__ bool start(const TreeParams &P, const TreeShare &sh, int BM, int BN) {
-    left = sh.end - sh.begin;
+    left = (int)min(sh.end - sh.begin, 0x7fffffffll);
     if (left <= 0) return false;
     s = sh.s;
     q = tree_seq(P, s, BM, BN, false);
@@ -159,7 +159,7 @@ struct TreeWalk {
     a = (int)(sh.rem - u * q.nt);
     m = (int)(u / P.Hkv);
     j = (int)(u - (long long)m * P.Hkv);
-    b = (int)min((long long)q.nt, a + left);
+    b = min(q.nt, a + left);
     return true;
   }
   __device__ __forceinline__ bool next(const TreeParams &P, int BM, int BN) {
@@ -175,7 +175,7 @@ struct TreeWalk {
       }
     }
     a = 0;
-    b = (int)min((long long)q.nt, left);
+    b = min(q.nt, left);
     return true;
   }
 };
@@ -430,18 +430,25 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   long long at = share.begin;  // tile index of the segment's first tile
   for (; more; at += w.b - w.a, more = w.next(P, C::BM, kTreeBN)) {
     const int prefix = w.q.len - w.q.n, rbase = w.m * C::BM, R = min(C::BM, w.q.n * P.g - rbase);
-    // Q fragments: a warp takes a row, a lane 4 neighbouring elements, which are
-    // one thread's (a0, a2) or (a1, a3) of one step
-    for (int r = warp; r < C::BM; r += kTreeWarps) {
-      uint32_t lo = 0, hi = 0;
-      float fac = 1.f;
+    // Q fragments: a warp takes a row, a lane 4 neighbouring elements, which are one
+    // thread's (a0, a2) or (a1, a3) of one step; a warp's rows are under way at once
+    constexpr int RW = C::BM / kTreeWarps;
+    uint2 qx[RW];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const int r = warp + k * kTreeWarps;
+      qx[k] = make_uint2(0u, 0u);
       if (r < R && lane < D / 4) {
-        const int i = (rbase + r) / P.g, h = w.j * P.g + (rbase + r) % P.g;
-        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(P.q) +
-                                                         (w.q.row0 + i) * P.q_tok + h * P.q_head + 4 * lane);
-        lo = x.x;
-        hi = x.y;
+        const int i = (rbase + r) / P.g, h = w.j * P.g + (rbase + r) - i * P.g;
+        qx[k] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(P.q) + (w.q.row0 + i) * P.q_tok +
+                                                 h * P.q_head + 4 * lane);
       }
+    }
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const int r = warp + k * kTreeWarps;
+      uint32_t lo = qx[k].x, hi = qx[k].y;
+      float fac = 1.f;
       if (C::kQuant && !P.q_f16) {
         float x[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
                       __uint_as_float(hi & 0xffff0000u)};
@@ -817,26 +824,40 @@ __global__ void __launch_bounds__(8 * D / 4) k_tree_join(const __grid_constant__
   const int R = min(BM, d.n * P.g - d.row_tile0);
   const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
   if (r >= R) return;
-  const int c0 = blockIdx.x;
+  // The lanes of a row (D / 4 of them) take a part each for the weights, 2^(m - M)
+  // of part c, then walk the parts together, the weights coming from their lanes.
+  constexpr int G = D / 4;
+  const int c0 = blockIdx.x, parts = d.last - c0 + 1, gl = threadIdx.x % G;
+  const unsigned gm = G == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
+  auto ml_of = [&](int k) {
+    if (k >= parts) return make_float2(-INFINITY, 0.f);
+    return *reinterpret_cast<const float2 *>(P.part_ml + ((int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * BM + r) * 2);
+  };
   float M = -INFINITY;
-  for (int c = c0; c <= d.last; ++c) {
-    const int slot = 2 * c + (c == c0 ? 1 : 0);
-    M = fmaxf(M, P.part_ml[((int64_t)slot * BM + r) * 2]);
-  }
+  for (int k = gl; k < parts; k += G) M = fmaxf(M, ml_of(k).x);
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(gm, M, o));
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int c = c0; c <= d.last; ++c) {
-    const int64_t at = (int64_t)(2 * c + (c == c0 ? 1 : 0)) * BM + r;
-    const float2 ml = *reinterpret_cast<const float2 *>(P.part_ml + at * 2);
-    const float4 v = *reinterpret_cast<const float4 *>(P.part + at * D + col);
+  for (int k0 = 0; k0 < parts; k0 += G) {
+    const float2 ml = ml_of(k0 + gl);
     const float f = ex2(ml.x - ref);
-    L = fmaf(ml.y, f, L);
-    acc.x = fmaf(v.x, f, acc.x);
-    acc.y = fmaf(v.y, f, acc.y);
-    acc.z = fmaf(v.z, f, acc.z);
-    acc.w = fmaf(v.w, f, acc.w);
+    float lsum = ml.y * f;
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) lsum += __shfl_xor_sync(gm, lsum, o);
+    L += lsum;
+    const int n = min(G, parts - k0);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const int64_t at = (int64_t)(2 * (c0 + k0 + k) + (k0 + k == 0 ? 1 : 0)) * BM + r;
+      const float4 v = *reinterpret_cast<const float4 *>(P.part + at * D + col);
+      const float fk = __shfl_sync(gm, f, k, G);
+      acc.x = fmaf(v.x, fk, acc.x);
+      acc.y = fmaf(v.y, fk, acc.y);
+      acc.z = fmaf(v.z, fk, acc.z);
+      acc.w = fmaf(v.w, fk, acc.w);
+    }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
   const int i = (d.row_tile0 + r) / P.g, h = d.j * P.g + (d.row_tile0 + r) % P.g;

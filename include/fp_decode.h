@@ -172,7 +172,7 @@ size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d);
  *   lse          device fp32 [Hq][T]
  *   work         workspace, 16-byte aligned, of at least fp_tree_attn_workspace
  *                bytes (work_bytes)
- * 1 <= max_q <= 256; n <= max_q; kv_len[s] >= n.  A sequence that breaks one of
+ * scale > 0; 1 <= max_q <= 256; n <= max_q; kv_len[s] >= n.  A sequence that breaks one of
  * the last two, or whose length passes max_pages*page, is left out (its rows of
  * out and lse stay as they were) and sets FP_ERR_RANGE, as does a page outside
  * the cache (its tokens are then unspecified).  Rows behind cu_q[nseq] stay as
