@@ -285,8 +285,8 @@ int fp_kv_create(void *k_pool, void *v_pool, float *k_scale, float *v_scale, int
   const uint32_t row = d * size_of(dtype), box = row < 128 ? row : 128;
   const uint64_t rows = (uint64_t)pages * Hkv * page;
   if (cudaGetDevice(&kv->device) != cudaSuccess ||
-      !make_byte_map(&kv->map[0], k_pool, row, rows, box, page < kTreeBN ? page : kTreeBN) ||
-      !make_byte_map(&kv->map[1], v_pool, row, rows, box, page < kTreeBN ? page : kTreeBN)) {
+      !make_byte_map(&kv->map[0], k_pool, row, rows, box, page < 64 ? page : 64) ||
+      !make_byte_map(&kv->map[1], v_pool, row, rows, box, page < 64 ? page : 64)) {
     delete kv;
     return FP_ERR_CUDA;
   }
@@ -372,11 +372,11 @@ bool tree_shape_ok(int nseq, int max_q, int Hq, int Hkv, int d) {
          (d == 64 || d == 128);
 }
 
-// Query rows of a unit for at most `rows` rows of a KV head, the tokens of a
-// tile and the CTAs that go with it.
+// Query rows of a unit for at most `rows` rows of a KV head, and the CTAs that go
+// with it.
 int tree_bm(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
-int tree_bn(int bm) { return bm <= 32 ? kTreeBN : kTcBN; }
-int tree_ctas(int bm) { return bm <= 32 ? 2 * sms() : sms(); }
+constexpr int kTreeLeastBN = 64;  // the shortest of all kernels' token tiles
+int tree_ctas(int bm) { return bm == 16 ? 2 * sms() : sms(); }
 
 struct TreeWork {
   size_t part, ml, desc, bytes;
@@ -418,7 +418,7 @@ template <int KIND, int D, int MT>
 int launch_tree(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st) {
   using C = TreeCfg<KIND, D, MT>;
   if (!allow_smem(k_tree<KIND, D, MT>, C::kSmem)) return FP_ERR_CUDA;
-  k_tree<KIND, D, MT><<<ctas, kTreeThreads, C::kSmem, st>>>(kv->map[0], kv->map[1], P, kv->g.pool[1]);
+  k_tree<KIND, D, MT><<<ctas, C::kThreads, C::kSmem, st>>>(kv->map[0], kv->map[1], P, kv->g.pool[1]);
   const int rc = status();
   return rc ? rc : launch_join<D>(P, C::BM, ctas, st);
 }
@@ -479,7 +479,7 @@ int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, 
   if (work_bytes < w.bytes) return FP_ERR_ARG;
   // no more CTAs than there can be tiles
   const double tiles = (double)nseq * ((max_q * g + bm - 1) / bm) * kv->g.heads *
-                       std::ceil((double)max_pages * kv->g.page / tree_bn(bm));
+                       std::ceil((double)max_pages * kv->g.page / kTreeLeastBN);
   const int ctas = tiles < most ? (tiles < 1 ? 1 : (int)tiles) : most;
   TreeParams P;
   P.scale[0] = kv->g.scale[0];

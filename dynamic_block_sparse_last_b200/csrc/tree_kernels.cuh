@@ -40,9 +40,6 @@
 
 namespace fpk {
 
-constexpr int kTreeBN = 64;          // tokens of a tile
-constexpr int kTreeWarps = 4;        // consumer warps, 16 tokens of a tile each
-constexpr int kTreeThreads = (kTreeWarps + 1) * 32;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct TreeDesc {       // a unit split over several CTAs, written by the first of them
@@ -236,11 +233,11 @@ __device__ __forceinline__ void tree_codes4(uint32_t w, uint32_t &lo, uint32_t &
 template <int KIND>
 __device__ __forceinline__ void tree_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (KIND == kKvBf16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -298,20 +295,35 @@ template <int KIND, int D, int MT>
 struct TreeCfg {
   static constexpr bool kQuant = KvCode<KIND>::kQuant;
   static constexpr int BM = 16 * MT;
+  // 16 rows: two CTAs per SM of four warps, 200 registers a thread; 32 rows: one of
+  // eight.  Over a quantised cache a warp takes 32 tokens at a time: its work per
+  // byte is larger, and two independent halves hide each other's latency.
+  static constexpr int kWarps = MT == 1 ? 4 : 8;
+  static constexpr int kCtas = MT == 1 ? 2 : 1;
+  static constexpr int kThreads = (MT == 1 ? kWarps + 1 : kWarps + 4) * 32;  // the producer; 32 rows: in a warpgroup of its own
+  // Registers of 32 rows: the block starts with 168 a thread (384 threads), and 2 x 128 x 216 + 128 x 56 = 62464 <= 384 x 168.
+  static constexpr int kRegs = 216, kRegsTma = 56;
+  static constexpr int TOK = kQuant && MT == 1 ? 32 : 16;  // tokens of a warp in a tile
+  static constexpr int BN = kWarps * TOK;                 // tokens of a tile
   static constexpr int RB = D * KvCode<KIND>::kBytes;     // bytes of a cached row
   static constexpr int kBoxB = RB < 128 ? RB : 128;       // bytes of a box row
   static constexpr int kBoxes = RB / kBoxB;
   static constexpr int E = 16 / KvCode<KIND>::kBytes;     // elements of 16 bytes
   static constexpr int kSteps = D / 16;
   static constexpr int VE = (kQuant && D == 128) ? 16 : 8;  // V columns of a thread's read
-  static constexpr int kTile = kTreeBN * RB;              // K (or V) bytes of a tile
+  static constexpr int kTile = BN * RB;                   // K (or V) bytes of a tile
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = kStage >= 32768 ? (MT == 1 ? 3 : 2) : (kStage >= 16384 ? 5 : 8);
-  static constexpr int kScaleOff = kStages * kStage;      // [stage][K, V][64] fp32
-  static constexpr int kQOff = kScaleOff + (kQuant ? kStages * 2 * kTreeBN * 4 : 0);  // [MT][steps][32] uint4
+  static constexpr int kStageAll = kStage + (kQuant ? 2 * BN * 4 : 0);  // with the scales
+  // as many as leave room for Q, obuf and the other CTA (227 KB an SM), 6 at most
+  static constexpr int kFit = (MT == 1 ? 99000 : 200000) / kStageAll, kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kScaleOff = kStages * kStage;      // [stage][K, V][BN] fp32
+  static constexpr int kQOff = kScaleOff + (kQuant ? kStages * 2 * BN * 4 : 0);  // [MT][steps][32] uint4
   static constexpr int kLd = D + 4;                       // row pitch of obuf (fp32)
   static constexpr int kOOff = kQOff + MT * kSteps * 512;
   static constexpr int kSmem = kOOff + BM * kLd * 4 + 1024;
+  // A row's reference moves when one of its scores passes it by more than this (log2
+  // units), as far as P's type goes: fp16 2^14, times V scales below 2; bf16 2^40.
+  static constexpr float kSlack = KIND == kKvBf16 ? 40.f : 14.f;
 };
 
 // Shared address of the 16-byte chunk `ch` of row r of a tile (TMA swizzle:
@@ -320,21 +332,21 @@ struct TreeCfg {
 template <typename C>
 __device__ __forceinline__ uint32_t tree_chunk(uint32_t tile, int r, int ch) {
   if constexpr (C::kBoxB == 128)
-    return tile + (ch >> 3) * (kTreeBN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    return tile + (ch >> 3) * (C::BN * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
   else
     return tile + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
 }
 
 template <int KIND, int D, int MT>
-__global__ void __launch_bounds__(kTreeThreads, 2)
+__global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIND, D, MT>::kCtas))
     k_tree(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
            const __grid_constant__ TreeParams P, const void *v_pool) {
   using C = TreeCfg<KIND, D, MT>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_full[C::kStages], bar_empty[C::kStages];
-  __shared__ long long warp_sum[kTreeThreads / 32];
+  __shared__ long long warp_sum[C::kThreads / 32];
   __shared__ TreeShare share;
-  __shared__ float red_m[kTreeWarps][C::BM], red_l[kTreeWarps][C::BM], row_scale[C::BM], fin_m[C::BM], fin_l[C::BM];
+  __shared__ float red_m[C::kWarps][C::BM], red_l[C::kWarps][C::BM], row_scale[C::BM], fin_m[C::BM], fin_l[C::BM];
   __shared__ int abort_sh, bad_sh;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -344,36 +356,38 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     bad_sh = 0;
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(smem_u32(&bar_full[i]), 1);
-      mbar_init(smem_u32(&bar_empty[i]), kTreeWarps);
+      mbar_init(smem_u32(&bar_empty[i]), C::kWarps);
     }
     fence_mbar_init();
   }
-  tree_share<kTreeThreads>(P, C::BM, kTreeBN, &share, warp_sum);
+  tree_share<C::kThreads>(P, C::BM, C::BN, &share, warp_sum);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   volatile int *abort_flag = &abort_sh;
   TreeWalk w;
-  bool more = w.start(P, share, C::BM, kTreeBN);
+  bool more = w.start(P, share, C::BM, C::BN);
 
-  if (warp == kTreeWarps) {
+  if (warp >= C::kWarps) {
     // ------------------------------------------------------------ producer
-    // A tile is 64 / min(page, 64) pieces, each of one page; lane i moves piece i.
-    const int piece = min(P.page, kTreeBN), pieces = kTreeBN / piece;
+    if constexpr (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsTma));
+    if (warp > C::kWarps) return;
+    // A tile is BN / min(page, 64) pieces, each of one page; lane i moves piece i.
+    const int piece = min(P.page, 64), pieces = C::BN / piece;
     if (lane == 0) {
       tma_prefetch_map(&tm_k);
       tma_prefetch_map(&tm_v);
     }
     int u = 0;
     bool ok = true;
-    for (; more && ok; more = w.next(P, C::BM, kTreeBN)) {
+    for (; more && ok; more = w.next(P, C::BM, C::BN)) {
       const int *tab = P.table + (int64_t)w.s * P.max_pages;
       int pg = 0;
-      const int p0 = w.a * kTreeBN + lane * piece;
+      const int p0 = w.a * C::BN + lane * piece;
       if (lane < pieces && p0 < w.q.len) pg = tab[p0 >> P.page_shift];
       for (int t = w.a; t < w.b; ++t, ++u) {
-        const int pos = t * kTreeBN + lane * piece;
+        const int pos = t * C::BN + lane * piece;
         const bool mine = lane < pieces && pos < w.q.len;
         const int now = pg;
-        const int nx = pos + kTreeBN;  // the next tile's page, ahead of its use
+        const int nx = pos + C::BN;  // the next tile's page, ahead of its use
         if (t + 1 < w.b && lane < pieces && nx < w.q.len) pg = tab[nx >> P.page_shift];
         const int st = u % C::kStages;
         if (u >= C::kStages) ok = mbar_wait(smem_u32(&bar_empty[st]), ((u / C::kStages) - 1) & 1, abort_flag, P.err);
@@ -395,13 +409,13 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
           const uint32_t dst = base + st * C::kStage + lane * piece * C::kBoxB;
 #pragma unroll
           for (int x = 0; x < C::kBoxes; ++x) {
-            tma_load_2d(dst + x * kTreeBN * 128, &tm_k, x * 128, row, bar);
-            tma_load_2d(dst + C::kTile + x * kTreeBN * 128, &tm_v, x * 128, row, bar);
+            tma_load_2d(dst + x * C::BN * 128, &tm_k, x * 128, row, bar);
+            tma_load_2d(dst + C::kTile + x * C::BN * 128, &tm_v, x * 128, row, bar);
           }
           if constexpr (C::kQuant) {
-            const uint32_t sd = base + C::kScaleOff + st * 2 * kTreeBN * 4 + lane * piece * 4;
+            const uint32_t sd = base + C::kScaleOff + st * 2 * C::BN * 4 + lane * piece * 4;
             bulk_load(sd, P.scale[0] + row, piece * 4, bar);
-            bulk_load(sd + kTreeBN * 4, P.scale[1] + row, piece * 4, bar);
+            bulk_load(sd + C::BN * 4, P.scale[1] + row, piece * 4, bar);
           }
         }
       }
@@ -421,22 +435,23 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
   }
 
   // -------------------------------------------------------------- consumers
+  if constexpr (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs));
   const int q4 = lane >> 2, c4 = lane & 3;
   const uint32_t qbase = base + C::kQOff;
   float *obuf = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)) + C::kOOff);
-  constexpr int NC = kTreeWarps * 32;
+  constexpr int NC = C::kWarps * 32;
   int u = 0;
   if (threadIdx.x == 0) P.desc[blockIdx.x].n = 0;
   long long at = share.begin;  // tile index of the segment's first tile
-  for (; more; at += w.b - w.a, more = w.next(P, C::BM, kTreeBN)) {
+  for (; more; at += w.b - w.a, more = w.next(P, C::BM, C::BN)) {
     const int prefix = w.q.len - w.q.n, rbase = w.m * C::BM, R = min(C::BM, w.q.n * P.g - rbase);
     // Q fragments: a warp takes a row, a lane 4 neighbouring elements, which are one
     // thread's (a0, a2) or (a1, a3) of one step; a warp's rows are under way at once
-    constexpr int RW = C::BM / kTreeWarps;
+    constexpr int RW = C::BM / C::kWarps;
     uint2 qx[RW];
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const int r = warp + k * kTreeWarps;
+      const int r = warp + k * C::kWarps;
       qx[k] = make_uint2(0u, 0u);
       if (r < R && lane < D / 4) {
         const int i = (rbase + r) / P.g, h = w.j * P.g + (rbase + r) - i * P.g;
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
     }
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const int r = warp + k * kTreeWarps;
+      const int r = warp + k * C::kWarps;
       uint32_t lo = qx[k].x, hi = qx[k].y;
       float fac = 1.f;
       if (C::kQuant && !P.q_f16) {
@@ -495,7 +510,8 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       m[mt][0] = m[mt][1] = -INFINITY;
       l[mt][0] = l[mt][1] = 0.f;
     }
-    int kexp = -126;
+    int kexp = -126;                   // V's scales are taken relative to 2^kexp: kinv = 2^-kexp,
+    float klim = 0.f, kinv = pow2i(126);  // and below klim = 2^(kexp + 1) (0 at first, so that the first one sets it)
     int bad = 0;
     for (int t = w.a; t < w.b; ++t, ++u) {
       const int st = u % C::kStages;
@@ -503,203 +519,241 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
       // barriers below have no time limit of their own); the results are lost
       if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&bar_full[st]), (u / C::kStages) & 1, abort_flag, P.err))) break;
       const uint32_t kt = base + st * C::kStage, vt = kt + C::kTile;
-      const int key0 = warp * 16;
-      const int pos0 = t * kTreeBN + key0;
-      const bool tail = pos0 + 16 > prefix;
-      // ---- scores of 16 tokens
-      float s[MT][2][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
-#pragma unroll
-      for (int h = 0; h < C::RB / 64; ++h) {
-        uint32_t kw[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 x = lds128(tree_chunk<C>(kt, key0 + 8 * i + q4, c4 + 4 * h));
-          kw[i][0] = x.x; kw[i][1] = x.y; kw[i][2] = x.z; kw[i][3] = x.w;
-        }
-#pragma unroll
-        for (int jj = 0; jj < C::E / 4; ++jj) {
-          const int step = h * (C::E / 4) + jj;
-          uint32_t b[2][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if constexpr (C::kQuant) {
-              tree_codes4<KIND>(KIND == kKvInt8 ? kw[i][jj] ^ 0x80808080u : kw[i][jj], b[i][0], b[i][1]);
-            } else {
-              b[i][0] = kw[i][2 * jj];
-              b[i][1] = kw[i][2 * jj + 1];
-            }
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            uint32_t a[4];
-            if constexpr (MT == 1) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) a[e] = qf[step][e];
-            } else {
-              const uint4 x = lds128(qbase + ((mt * C::kSteps + step) * 32 + lane) * 16);
-              a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
-            }
-            tree_mma<KIND>(s[mt][0], a, b[0][0], b[0][1]);
-            tree_mma<KIND>(s[mt][1], a, b[1][0], b[1][1]);
-          }
-        }
-      }
-      // ---- scales and masks
-      float vs[4] = {1.f, 1.f, 1.f, 1.f};  // V scales of tokens 2c, 2c+1, 8+2c, 9+2c
-      if constexpr (C::kQuant) {
-        const uint32_t sc = base + C::kScaleOff + st * 2 * kTreeBN * 4 + (key0 + 2 * c4) * 4;
-        const uint2 k0 = lds64(sc), k1 = lds64(sc + 32);
-        const uint2 v0 = lds64(sc + kTreeBN * 4), v1 = lds64(sc + kTreeBN * 4 + 32);
-        const float ks[4] = {__uint_as_float(k0.x), __uint_as_float(k0.y), __uint_as_float(k1.x), __uint_as_float(k1.y)};
-        vs[0] = __uint_as_float(v0.x); vs[1] = __uint_as_float(v0.y);
-        vs[2] = __uint_as_float(v1.x); vs[3] = __uint_as_float(v1.y);
+      constexpr int NT = C::TOK / 8, NB = C::TOK / 16;  // 8-token tiles of S, 16-token steps of P V
+      const int key0 = warp * C::TOK;
+      const int pos0 = t * C::BN + key0;
+      // compiled once for tokens that every row sees and once for the others
+      auto step = [&](auto tail_tag) __attribute__((always_inline)) {
+        constexpr bool tail = decltype(tail_tag)::value;
+        // ---- scores
+        float s[MT][NT][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][i][e] *= ks[2 * i + (e & 1)] * rs[mt][e >> 1];
-      } else {
+            for (int e = 0; e < 4; ++e) s[mt][i][e] = 0.f;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < C::RB / 64; ++h) {
+          uint32_t kw[NT][4];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < NT; ++i) {
+            const uint4 x = lds128(tree_chunk<C>(kt, key0 + 8 * i + q4, c4 + 4 * h));
+            kw[i][0] = x.x; kw[i][1] = x.y; kw[i][2] = x.z; kw[i][3] = x.w;
+          }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s[mt][i][e] *= rs[mt][e >> 1];
-      }
-      uint32_t hide = 0;  // bit (mt * 8 + i * 4 + e): not visible
-      if (tail) {
+          for (int jj = 0; jj < C::E / 4; ++jj) {
+            const int step = h * (C::E / 4) + jj;
+            uint32_t b[NT][2];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              if constexpr (C::kQuant) {
+                tree_codes4<KIND>(KIND == kKvInt8 ? kw[i][jj] ^ 0x80808080u : kw[i][jj], b[i][0], b[i][1]);
+              } else {
+                b[i][0] = kw[i][2 * jj];
+                b[i][1] = kw[i][2 * jj + 1];
+              }
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t a[4];
+              if constexpr (MT == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[e] = qf[step][e];
+              } else {
+                const uint4 x = lds128(qbase + ((mt * C::kSteps + step) * 32 + lane) * 16);
+                a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
+              }
+#pragma unroll
+              for (int i = 0; i < NT; ++i) tree_mma<KIND>(s[mt][i], a, b[i][0], b[i][1]);
+            }
+          }
+        }
+        // ---- scales and masks; a thread has tokens 8i + 2c, 8i + 2c + 1 of rows q, q + 8
+        float vs[2 * NT];
+        const uint32_t sc = base + C::kScaleOff + st * 2 * C::BN * 4 + (key0 + 2 * c4) * 4;
+        if constexpr (C::kQuant) {
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            const uint2 k = lds64(sc + 32 * i);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[mt][i][e] *= __uint_as_float(e & 1 ? k.y : k.x) * rs[mt][e >> 1];
+            const uint2 v = lds64(sc + C::BN * 4 + 32 * i);
+            vs[2 * i] = __uint_as_float(v.x);
+            vs[2 * i + 1] = __uint_as_float(v.y);
+          }
+        } else {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[mt][i][e] *= rs[mt][e >> 1];
+        }
+        [[maybe_unused]] uint32_t hide = 0;  // bit ((mt * NT + i) * 4 + e): not visible
+        if constexpr (tail) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+              const int i = min((rbase + 16 * mt + 8 * hh + q4) / P.g, w.q.n - 1);
+#pragma unroll
+              for (int k = 0; k < 2 * NT; ++k) {
+                const int pos = pos0 + 8 * (k >> 1) + 2 * c4 + (k & 1), e = 2 * hh + (k & 1);
+                const bool vis = pos < prefix || (pos < w.q.len && tree_sees(P, w.q, i, pos - prefix));
+                if (!vis) {
+                  s[mt][k >> 1][e] = -INFINITY;
+                  hide |= 1u << ((mt * NT + (k >> 1)) * 4 + e);
+                }
+              }
+            }
+          if constexpr (C::kQuant) {
+#pragma unroll
+            for (int k = 0; k < 2 * NT; ++k)
+              if (pos0 + 8 * (k >> 1) + 2 * c4 + (k & 1) >= w.q.len) vs[k] = 0.f;
+          }
+        }
+        // ---- softmax against the rows' references.  In the common case no thread's
+        // values ask for more than a vote; only then do the four lanes of a row agree
+        // on its largest score, and the warp on the largest V scale.
+        float mxl[MT][2];
+        bool ask = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const int i = min((rbase + 16 * mt + 8 * hh + q4) / P.g, w.q.n - 1);
+            float mx = fmaxf(s[mt][0][2 * hh], s[mt][0][2 * hh + 1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int pos = pos0 + 8 * (e >> 1) + 2 * c4 + (e & 1);
-              const bool vis = pos < prefix || (pos < w.q.len && tree_sees(P, w.q, i, pos - prefix));
-              if (!vis) {
-                s[mt][e >> 1][2 * hh + (e & 1)] = -INFINITY;
-                hide |= 1u << (mt * 8 + (e >> 1) * 4 + 2 * hh + (e & 1));
-              }
-            }
+            for (int i = 1; i < NT; ++i) mx = fmaxf(mx, fmaxf(s[mt][i][2 * hh], s[mt][i][2 * hh + 1]));
+            mxl[mt][hh] = mx;
+            ask |= mx > m[mt][hh] + C::kSlack;
           }
+        float vmx = 0.f;
+        if constexpr (C::kQuant) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (pos0 + 8 * (e >> 1) + 2 * c4 + (e & 1) >= w.q.len) vs[e] = 0.f;
-      }
-      // ---- softmax with the running maximum of this warp's tokens
-      float kfac = 1.f;
-      bool moved = false;
-      if constexpr (C::kQuant) {
-        float mx = fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int e = mx < INFINITY ? min((int)(__float_as_uint(mx) >> 23) - 127, 126) : -127;  // NaN scales do not count
-        if (e > kexp + 4) {  // uniform in the warp; probabilities times scales stay below 2^5
-          kfac = e - kexp > 126 ? 0.f : pow2i(kexp - e);
-          kexp = e;
-          moved = true;
+          for (int k = 0; k < 2 * NT; ++k) vmx = fmaxf(vmx, vs[k]);
+          ask |= vmx >= klim && vmx < INFINITY;  // a NaN scale does not count
         }
-        const float kinv = pow2i(-kexp);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vs[i] *= kinv;
-      }
-      uint32_t pa[MT][4];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float al[2];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float mx = fmaxf(fmaxf(s[mt][0][2 * hh], s[mt][0][2 * hh + 1]), fmaxf(s[mt][1][2 * hh], s[mt][1][2 * hh + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[mt][hh], mx);
-          al[hh] = mn > m[mt][hh] ? ex2(m[mt][hh] - mn) : 1.f;
-          moved |= mn > m[mt][hh];
-          m[mt][hh] = mn;
-          const float ref = mn == -INFINITY ? 0.f : mn;
-          float p[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = ex2(s[mt][e >> 1][2 * hh + (e & 1)] - ref);
-          l[mt][hh] = l[mt][hh] * al[hh] + ((p[0] + p[1]) + (p[2] + p[3]));
+        if (__any_sync(0xffffffffu, ask)) {
+          float kfac = 1.f;
           if constexpr (C::kQuant) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] *= vs[e];
-              if (tail && (hide >> (mt * 8 + (e >> 1) * 4 + 2 * hh + (e & 1))) & 1u) p[e] = 0.f;
+            vmx = vmx < INFINITY ? vmx : 0.f;
+            vmx = redux_max_f32(vmx);
+            if (vmx >= klim) {  // V's scales relative to 2^kexp stay below 2
+              const int e = min((int)(__float_as_uint(vmx) >> 23) - 127, 125);
+              kfac = e - kexp > 126 ? 0.f : pow2i(kexp - e);
+              kexp = e;
+              klim = pow2i(e + 1);
+              kinv = pow2i(-e);
             }
           }
-          pa[mt][hh] = KIND == kKvBf16 ? pack_bf16x2(p[0], p[1]) : pack_f16x2(p[0], p[1]);
-          pa[mt][2 + hh] = KIND == kKvBf16 ? pack_bf16x2(p[2], p[3]) : pack_f16x2(p[2], p[3]);
-        }
-        al[0] *= kfac;
-        al[1] *= kfac;
-        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i)
+          for (int mt = 0; mt < MT; ++mt) {
+            float al[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[mt][i][e] *= al[e >> 1];
-        }
-      }
-      // ---- O += P V
-#pragma unroll
-      for (int x = 0; x < C::kBoxes; ++x) {
-        uint32_t vw[4][C::VE * KvCode<KIND>::kBytes / 4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = key0 + 8 * (e >> 1) + 2 * c4 + (e & 1);
-          if constexpr (C::VE * KvCode<KIND>::kBytes == 16) {
-            const uint4 y = lds128(tree_chunk<C>(vt, r, q4 + 8 * x));
-            vw[e][0] = y.x; vw[e][1] = y.y; vw[e][2] = y.z; vw[e][3] = y.w;
-          } else {
-            const uint2 y = lds64(tree_chunk<C>(vt, r, q4 >> 1) + (q4 & 1) * 8);
-            vw[e][0] = y.x; vw[e][1] = y.y;
-          }
-        }
-        if (tail) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int pos = pos0 + 8 * (e >> 1) + 2 * c4 + (e & 1);
-#pragma unroll
-            for (int k = 0; k < C::VE * KvCode<KIND>::kBytes / 4; ++k) {
-              if (pos >= w.q.len) vw[e][k] = 0u;
-              else if (pos >= prefix) vw[e][k] = tree_clean<KIND>(vw[e][k], bad);
+            for (int hh = 0; hh < 2; ++hh) {
+              float mx = mxl[mt][hh];
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+              const float mn = mx > m[mt][hh] + C::kSlack ? mx : m[mt][hh];
+              al[hh] = mn > m[mt][hh] ? ex2(m[mt][hh] - mn) : 1.f;
+              m[mt][hh] = mn;
+              l[mt][hh] *= al[hh];
+              al[hh] *= kfac;
             }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[mt][i][e] *= al[e >> 1];
           }
         }
         if constexpr (C::kQuant) {
 #pragma unroll
-          for (int k = 0; k < C::VE / 4; ++k) {
-            uint32_t b0[4], b1[4];  // columns 4k .. 4k+3
-            const uint32_t fl = KIND == kKvInt8 ? 0x80808080u : 0u;
-            tree_codes4<KIND>(prmt(vw[0][k], vw[1][k], 0x5140u) ^ fl, b0[0], b0[1]);
-            tree_codes4<KIND>(prmt(vw[0][k], vw[1][k], 0x7362u) ^ fl, b0[2], b0[3]);
-            tree_codes4<KIND>(prmt(vw[2][k], vw[3][k], 0x5140u) ^ fl, b1[0], b1[1]);
-            tree_codes4<KIND>(prmt(vw[2][k], vw[3][k], 0x7362u) ^ fl, b1[2], b1[3]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) tree_mma<KIND>(o[mt][4 * k + i], pa[mt], b0[i], b1[i]);
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t sel = i ? 0x7632u : 0x5410u;
-              const uint32_t b0 = prmt(vw[0][k], vw[1][k], sel), b1 = prmt(vw[2][k], vw[3][k], sel);
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) tree_mma<KIND>(o[mt][8 * x + 2 * k + i], pa[mt], b0, b1);
-            }
+          for (int k = 0; k < 2 * NT; ++k) vs[k] *= kinv;
         }
-      }
+        uint32_t pa[MT][NB][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float ref = m[mt][hh] == -INFINITY ? 0.f : m[mt][hh];
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              float p0 = ex2(s[mt][i][2 * hh] - ref), p1 = ex2(s[mt][i][2 * hh + 1] - ref);
+              sum += p0 + p1;
+              if constexpr (C::kQuant) {
+                p0 *= vs[2 * i];
+                p1 *= vs[2 * i + 1];
+                if constexpr (tail) {  // a hidden token's scale may be a NaN
+                  if ((hide >> ((mt * NT + i) * 4 + 2 * hh)) & 1u) p0 = 0.f;
+                  if ((hide >> ((mt * NT + i) * 4 + 2 * hh + 1)) & 1u) p1 = 0.f;
+                }
+              }
+              pa[mt][i >> 1][2 * (i & 1) + hh] = KIND == kKvBf16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+            }
+            l[mt][hh] += sum;
+          }
+        // ---- O += P V
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+          for (int x = 0; x < C::kBoxes; ++x) {
+            constexpr int VW = C::VE * KvCode<KIND>::kBytes / 4;
+            uint32_t vw[4][VW];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int r = key0 + 16 * kb + 8 * (e >> 1) + 2 * c4 + (e & 1);
+              if constexpr (VW == 4) {
+                const uint4 y = lds128(tree_chunk<C>(vt, r, q4 + 8 * x));
+                vw[e][0] = y.x; vw[e][1] = y.y; vw[e][2] = y.z; vw[e][3] = y.w;
+              } else {
+                const uint2 y = lds64(tree_chunk<C>(vt, r, q4 >> 1) + (q4 & 1) * 8);
+                vw[e][0] = y.x; vw[e][1] = y.y;
+              }
+            }
+            if constexpr (tail) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int pos = pos0 + 16 * kb + 8 * (e >> 1) + 2 * c4 + (e & 1);
+#pragma unroll
+                for (int k = 0; k < VW; ++k) {
+                  if (pos >= w.q.len) vw[e][k] = 0u;
+                  else if (pos >= prefix) vw[e][k] = tree_clean<KIND>(vw[e][k], bad);
+                }
+              }
+            }
+            if constexpr (C::kQuant) {
+#pragma unroll
+              for (int k = 0; k < C::VE / 4; ++k) {
+                uint32_t b0[4], b1[4];  // columns 4k .. 4k+3
+                const uint32_t fl = KIND == kKvInt8 ? 0x80808080u : 0u;
+                tree_codes4<KIND>(prmt(vw[0][k], vw[1][k], 0x5140u) ^ fl, b0[0], b0[1]);
+                tree_codes4<KIND>(prmt(vw[0][k], vw[1][k], 0x7362u) ^ fl, b0[2], b0[3]);
+                tree_codes4<KIND>(prmt(vw[2][k], vw[3][k], 0x5140u) ^ fl, b1[0], b1[1]);
+                tree_codes4<KIND>(prmt(vw[2][k], vw[3][k], 0x7362u) ^ fl, b1[2], b1[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) tree_mma<KIND>(o[mt][4 * k + i], pa[mt][kb], b0[i], b1[i]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t sel = i ? 0x7632u : 0x5410u;
+                  const uint32_t b0 = prmt(vw[0][k], vw[1][k], sel), b1 = prmt(vw[2][k], vw[3][k], sel);
+#pragma unroll
+                  for (int mt = 0; mt < MT; ++mt) tree_mma<KIND>(o[mt][8 * x + 2 * k + i], pa[mt][kb], b0, b1);
+                }
+            }
+          }
+      };
+      if (pos0 + C::TOK > prefix) step(std::true_type{});
+      else step(std::false_type{});
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
     }
@@ -725,18 +779,18 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         const int r = 16 * mt + 8 * hh + q4;
         float M = red_m[0][r];
 #pragma unroll
-        for (int k = 1; k < kTreeWarps; ++k) M = fmaxf(M, red_m[k][r]);
+        for (int k = 1; k < C::kWarps; ++k) M = fmaxf(M, red_m[k][r]);
         const float ref = M == -INFINITY ? 0.f : M;
         float L = 0.f;
 #pragma unroll
-        for (int k = 0; k < kTreeWarps; ++k) L += red_l[k][r] * ex2(red_m[k][r] - ref);
+        for (int k = 0; k < C::kWarps; ++k) L += red_l[k][r] * ex2(red_m[k][r] - ref);
         f[mt][hh] = ex2(m[mt][hh] - ref) * (C::kQuant ? pow2i(kexp) : 1.f);
         if (warp == 0 && c4 == 0) {
           fin_m[r] = M;
           fin_l[r] = L;
         }
       }
-    for (int k = 0; k < kTreeWarps; ++k) {
+    for (int k = 0; k < C::kWarps; ++k) {
       if (warp == k) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
@@ -779,7 +833,7 @@ __global__ void __launch_bounds__(kTreeThreads, 2)
         float *vv = reinterpret_cast<float *>(&v);
         for (int jj = 0; jj < w.q.n; ++jj) {
           const int pos = prefix + jj;
-          if (pos < w.a * kTreeBN || pos >= w.b * kTreeBN || !tree_sees(P, w.q, i, jj)) continue;
+          if (pos < w.a * C::BN || pos >= w.b * C::BN || !tree_sees(P, w.q, i, jj)) continue;
           for (int e = 0; e < 4; ++e) {
             const float y = tree_v_value<KIND, D>(P, v_pool, w.s, w.j, pos, col + e);
             if (!(fabsf(y) < INFINITY)) vv[e] += y;
