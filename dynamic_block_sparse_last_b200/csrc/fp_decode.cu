@@ -1,8 +1,8 @@
 // fp_decode.cu -- host side of include/fp_decode.h: argument checks, the
 // rotary frequencies, tensor maps and launches.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
 #include <new>
 
 #include "fp_decode.h"
@@ -34,15 +34,15 @@ int status() { return cudaGetLastError() == cudaSuccess ? FP_OK : FP_ERR_CUDA; }
 
 // Multiprocessors of the current device, looked up once per device.
 int sms() {
-  static int n[128] = {};
+  static std::atomic<int> n[128];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return 0;
-  if (!n[dev]) {
-    int v = 0;
+  int v = n[dev].load(std::memory_order_relaxed);
+  if (!v) {
     if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    n[dev] = v;
+    n[dev].store(v, std::memory_order_relaxed);
   }
-  return n[dev];
+  return v;
 }
 
 int size_of(int dtype) {
@@ -210,14 +210,27 @@ bool on_device(const fp_kv *kv) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
 }
 
-// Heads of a block of 64 tokens: all of them for many tokens, so that the
-// slots are looked up once; fewer until there are about four blocks per
-// multiprocessor.
-int kv_group(int heads, int T) {
-  const int64_t blocks = (T + kKvTokens - 1) / kKvTokens;
-  int64_t groups = (4 * (int64_t)sms() + blocks - 1) / blocks;
+// Tokens and heads of a block: 32 tokens of all heads, so that the slots are looked
+// up once for them, while that makes about eight blocks per multiprocessor (enough to
+// fill it); with less work, fewer heads, and then 16 tokens.
+struct KvSplit {
+  int shift, group;
+  dim3 grid;
+};
+KvSplit kv_split(int heads, int T) {
+  KvSplit s;
+  const int64_t want = 8 * (int64_t)sms();
+  s.shift = 5;
+  int64_t blocks = (T + 31) / 32;
+  if (blocks * heads < want) {
+    s.shift = 4;
+    blocks = (T + 15) / 16;
+  }
+  int64_t groups = (want + blocks - 1) / blocks;
   if (groups > heads) groups = heads;
-  return (int)((heads + groups - 1) / groups);
+  s.group = (int)((heads + groups - 1) / groups);
+  s.grid = dim3((unsigned)blocks, (unsigned)((heads + s.group - 1) / s.group));
+  return s;
 }
 
 template <int KIND, typename T>
@@ -317,11 +330,12 @@ int fp_kv_write(const fp_kv *kv, const void *k, int64_t k_tok, int64_t k_head, c
   P.head[1] = v_head;
   P.slots = slots;
   P.T = T;
-  P.group = kv_group(kv->g.heads, T);
+  const KvSplit split = kv_split(kv->g.heads, T);
+  P.group = split.group;
+  P.tok_shift = split.shift;
   P.err = library_error_word();
   if (!P.err) return FP_ERR_CUDA;
-  const dim3 grid((T + kKvTokens - 1) / kKvTokens, (kv->g.heads + P.group - 1) / P.group);
-  return launch_kv(kv->dtype, dtype, P, kv->d, grid, static_cast<cudaStream_t>(stream));
+  return launch_kv(kv->dtype, dtype, P, kv->d, split.grid, static_cast<cudaStream_t>(stream));
 }
 
 int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const int32_t *cu, const int32_t *first,
@@ -351,11 +365,12 @@ int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const
   P.max_pages = max_pages;
   P.nseq = nseq;
   P.T = T;
-  P.group = kv_group(kv->g.heads, T);
+  const KvSplit split = kv_split(kv->g.heads, T);
+  P.group = split.group;
+  P.tok_shift = split.shift;
   P.err = library_error_word();
   if (!P.err) return FP_ERR_CUDA;
-  const dim3 grid((T + kKvTokens - 1) / kKvTokens, (kv->g.heads + P.group - 1) / P.group);
-  return launch_kv(kv->dtype, dtype, P, kv->d, grid, static_cast<cudaStream_t>(stream));
+  return launch_kv(kv->dtype, dtype, P, kv->d, split.grid, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
@@ -376,7 +391,7 @@ bool tree_shape_ok(int nseq, int max_q, int Hq, int Hkv, int d) {
 // with it.
 int tree_bm(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
 constexpr int kTreeLeastBN = 64;  // the shortest of all kernels' token tiles
-int tree_ctas(int bm) { return bm == 16 ? 2 * sms() : sms(); }
+int tree_ctas(int bm, int d) { return bm == 16 || (bm == 32 && d == 64) ? 2 * sms() : sms(); }
 
 struct TreeWork {
   size_t part, ml, desc, bytes;
@@ -390,12 +405,17 @@ TreeWork tree_work(int ctas, int bm, int d) {
   return w;
 }
 
-// Raises the kernel's shared-memory limit once per device and context-less: the
-// call is cheap enough to be made before every launch, and a reset device
-// forgets it.
+// Raises a kernel's shared-memory limit, once in a context; `where` is the kernel's
+// own record of the contexts it was raised in, by device.
 template <typename K>
-bool allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+bool allow_smem(K kernel, int bytes, std::atomic<void *> (&where)[128]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 128) return false;
+  void *ctx = library_context();
+  if (ctx && where[dev].load(std::memory_order_relaxed) == ctx) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  where[dev].store(ctx, std::memory_order_relaxed);
+  return true;
 }
 
 // The parts of split units are added up by a launch of its own, which may be
@@ -417,7 +437,8 @@ int launch_join(const TreeParams &P, int bm, int ctas, cudaStream_t st) {
 template <int KIND, int D, int MT>
 int launch_tree(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st) {
   using C = TreeCfg<KIND, D, MT>;
-  if (!allow_smem(k_tree<KIND, D, MT>, C::kSmem)) return FP_ERR_CUDA;
+  static std::atomic<void *> raised[128];
+  if (!allow_smem(k_tree<KIND, D, MT>, C::kSmem, raised)) return FP_ERR_CUDA;
   k_tree<KIND, D, MT><<<ctas, C::kThreads, C::kSmem, st>>>(kv->map[0], kv->map[1], P, kv->g.pool[1]);
   const int rc = status();
   return rc ? rc : launch_join<D>(P, C::BM, ctas, st);
@@ -426,7 +447,8 @@ int launch_tree(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st)
 template <int KIND, int D, bool PAIR>
 int launch_tree_tc(const fp_kv *kv, const TreeParams &P, int ctas, cudaStream_t st) {
   using C = TcCfg<KIND, D, PAIR>;
-  if (!allow_smem(k_tree_tc<KIND, D, PAIR>, C::kSmem)) return FP_ERR_CUDA;
+  static std::atomic<void *> raised[128];
+  if (!allow_smem(k_tree_tc<KIND, D, PAIR>, C::kSmem, raised)) return FP_ERR_CUDA;
   k_tree_tc<KIND, D, PAIR><<<ctas, kTcThreads, C::kSmem, st>>>(kv->map[0], kv->map[1], P, kv->g.pool[1]);
   const int rc = status();
   return rc ? rc : launch_join<D>(P, C::BM, ctas, st);
@@ -454,7 +476,7 @@ size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d) {
   if (!tree_shape_ok(nseq, max_q, Hq, Hkv, d)) return 0;
   if (!sms()) return 0;
   const int bm = tree_bm(max_q * (Hq / Hkv));
-  return tree_work(tree_ctas(bm), bm, d).bytes;
+  return tree_work(tree_ctas(bm, d), bm, d).bytes;
 }
 
 int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, int dtype, int T, int Hq,
@@ -474,7 +496,7 @@ int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, 
   if (!on_device(kv)) return FP_ERR_ARG;
   if (!sms()) return FP_ERR_CUDA;
   const int g = Hq / kv->g.heads, bm = tree_bm(max_q * g);
-  const int most = tree_ctas(bm);
+  const int most = tree_ctas(bm, kv->d);
   const TreeWork w = tree_work(most, bm, kv->d);
   if (work_bytes < w.bytes) return FP_ERR_ARG;
   // no more CTAs than there can be tiles

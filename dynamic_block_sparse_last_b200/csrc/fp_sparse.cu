@@ -182,6 +182,7 @@ bool make_map_split(CUtensorMap *m, const float *ptr, uint64_t rows) {
 namespace fpk {
 
 int *library_error_word() { return device_error_word(); }
+void *library_context() { return current_context(); }
 
 bool make_byte_map(CUtensorMap *m, const void *ptr, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
                    uint32_t box_rows) {

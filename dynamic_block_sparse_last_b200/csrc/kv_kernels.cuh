@@ -2,13 +2,21 @@
 // written to their slots, and read back.
 //
 // A row is the d values of one token in one head: scale = M / c, code =
-// round(c x / M), M = max|x|; c = 127 (int8) or 448 (e4m3).  The quotient is
-// formed by one multiplication with c / M (error below 2^-21 of it) and only
-// where that leaves the rounding open, near a value half way between two codes,
-// by the correctly rounded division (c x) / M, so the code is that of the
-// division for every row at about a third of its instructions.
+// round(c x / M), M = max|x|; c = 127 (int8) or 448 (e4m3).
 //
-// Bound: memory, each byte once.  A block takes 64 neighbouring tokens and a
+// The code without a division per element: with v = c / M to 2^-21.9, the quotient
+// q = c x / M lies between x v (1 - 2^-20) and x v (1 + 2^-20), both within 2^-19.4 of
+// it (relative to q), and rounding is monotone, so where both round to the same code
+// that is q's code.  Where they do not, a border t of two codes lies between them.  For
+// bf16 and fp16 rows q then is t, and the even code is the answer, since a quotient that
+// is not a border is further than 2^-19 from it: with x = b 2^i, M = a 2^j, a, b < 2^11,
+//   int8  q = 127 b 2^n / a, t = T / 2 (T odd, < 2^8): q - t = (254 b 2^n - a T) / 2a; if
+//         not 0, at least 1/2a, 1/(aT) of t, for n >= 0, else 2^n / 2a, 1/(254 b) of q;
+//   e4m3  q = 7 b 2^n / a, t = T 2^k (T odd, < 2^5): at least 2^min(n,k) / a, which is
+//         1/(7 b) of q or 1/(aT) of t.
+// fp32 rows take the correctly rounded division there.
+//
+// Bound: memory, each byte once.  A block takes some neighbouring tokens and a
 // group of heads: it looks the tokens' slots up once, into shared memory, and
 // then moves rows in 16-byte vectors, several rows in flight per thread.
 #pragma once
@@ -20,7 +28,7 @@
 
 namespace fpk {
 
-constexpr int kKvTokens = 64;    // tokens of a block
+constexpr int kKvTokens = 64;    // most tokens of a block
 constexpr int kKvThreads = 256;
 
 struct KvGeom {
@@ -36,6 +44,7 @@ struct KvWriteParams {
   int64_t tok[2], head[2];
   const int64_t *slots;
   int T, group;        // heads of a block
+  int tok_shift;       // log2 of its tokens
   int *err;
 };
 
@@ -44,7 +53,7 @@ struct KvReadParams {
   void *out[2];
   int64_t tok[2], head[2];
   const int *table, *cu, *first;
-  int max_pages, nseq, T, group;
+  int max_pages, nseq, T, group, tok_shift;
   int *err;
 };
 
@@ -57,46 +66,90 @@ struct KvCode {
   static constexpr float kTop = KIND == kKvInt8 ? 127.f : 448.f;
 };
 
-// Four codes of the quotients y (c x / M by multiplication), exact ones where
-// the rounding is open.
+// Four codes, packed: those of x vlo and of x vhi.
 template <int KIND>
-__device__ __forceinline__ uint32_t kv_codes4(const float *x, float inv, float M) {
-  constexpr float C = KvCode<KIND>::kTop;
-  float y[4];
-  bool open = false;
+__device__ __forceinline__ uint32_t kv_codes4(const float *x, float v) {
   if constexpr (KIND == kKvInt8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = x[i] * inv;
-      // |y| <= 127.0001, off by at most 127 * 2^-21 = 6.1e-5
-      open |= fabsf(fabsf(y[i] - rintf(y[i])) - 0.5f) < 1e-4f;
-    }
+    // x v + 1.5 2^23, rounded once: the integer (half to even) in the low bits
+    const uint64_t v2 = f2_pack(v, v), big = f2_pack(12582912.f, 12582912.f);
+    float y[4];
+    f2_unpack(f2_fma(f2_pack(x[0], x[1]), v2, big), y[0], y[1]);
+    f2_unpack(f2_fma(f2_pack(x[2], x[3]), v2, big), y[2], y[3]);
+    const uint32_t lo = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
+    const uint32_t hi = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      y[i] = x[i] * inv;
-      // Half way between two normal codes the 20 bits below the kept 3 are
-      // 0x80000 (2^-24 of the value a step); below 2^-6 the codes are 2^-9
-      // apart, and the division is always made.
-      const uint32_t low = __float_as_uint(y[i]) & 0xfffffu;
-      open |= (low - (0x80000u - 64u)) < 128u || (fabsf(y[i]) < 0.015625f && y[i] != 0.f);
-    }
-  }
-  if (open) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = __fdiv_rn(C * x[i], M);
-  }
-  if constexpr (KIND == kKvInt8) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w |= (static_cast<uint32_t>(__float2int_rn(y[i])) & 0xffu) << (8 * i);
+    const uint64_t v2 = f2_pack(v, v);
+    float y[4];
+    f2_unpack(f2_mul(f2_pack(x[0], x[1]), v2), y[0], y[1]);
+    f2_unpack(f2_mul(f2_pack(x[2], x[3]), v2), y[2], y[3]);
+    uint32_t w;
+    asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
+        "mov.b32 %0, {l, h};\n\t}"
+        : "=r"(w)
+        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]));
     return w;
-  } else {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
-    return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
   }
+}
+
+// One code of a correctly rounded quotient.
+template <int KIND>
+__device__ __forceinline__ uint32_t kv_code_exact(float x, float M) {
+  const float y = __fdiv_rn(KvCode<KIND>::kTop * x, M);
+  if constexpr (KIND == kKvInt8) return static_cast<uint32_t>(__float2int_rn(y)) & 0xffu;
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(y));
+  return c & 0xffu;
+}
+
+// The codes of one lane's elements of a row (EXACT: rows of fp32).
+template <int KIND, int V, bool EXACT>
+__device__ __forceinline__ void kv_quantise(const float *x, float M, uint32_t *code) {
+  const float v = __fdividef(KvCode<KIND>::kTop, M);  // 1e-30 < M < 1e30
+  const float vlo = v * (1.f - 9.5367431640625e-07f), vhi = v * (1.f + 9.5367431640625e-07f);
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    const uint32_t lo = kv_codes4<KIND>(x + i, vlo), hi = kv_codes4<KIND>(x + i, vhi);
+    if constexpr (EXACT) {
+      code[i / 4] = lo;
+      if (lo != hi) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w |= kv_code_exact<KIND>(x[i + e], M) << (8 * e);
+        code[i / 4] = w;
+      }
+    } else {
+      // the even code of each byte's two (the same one mostly): hi where lo is odd
+      const uint32_t odd = (lo & 0x01010101u) * 255u;
+      code[i / 4] = (hi & odd) | (lo & ~odd);
+    }
+  }
+}
+
+// The largest magnitude of a lane's 16 bytes, as fp32 bits: a NaN's are above an
+// infinity's, so anything not finite is seen.
+template <typename T>
+__device__ __forceinline__ uint32_t kv_max_bits(const uint4 &r) {
+  if constexpr (sizeof(T) == 4) {
+    return max(max(r.x & 0x7fffffffu, r.y & 0x7fffffffu), max(r.z & 0x7fffffffu, r.w & 0x7fffffffu));
+  } else {
+    constexpr uint32_t A = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(r.x & A, r.y & A), __vmaxu2(r.z & A, r.w & A));  // pairs of 16-bit magnitudes
+  }
+}
+template <typename T, int L>
+__device__ __forceinline__ float kv_row_max(const uint4 &r) {
+  uint32_t m = kv_max_bits<T>(r);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const uint32_t y = __shfl_xor_sync(0xffffffffu, m, o);
+    if constexpr (sizeof(T) == 4) m = max(m, y);
+    else m = __vmaxu2(m, y);
+  }
+  if constexpr (sizeof(T) == 4) return __uint_as_float(m);
+  m = max(m & 0xffffu, m >> 16);
+  if constexpr (std::is_same<T, __half>::value) return __half2float(__ushort_as_half(static_cast<unsigned short>(m)));
+  return __uint_as_float(m << 16);
 }
 
 // Values of four codes.
@@ -117,16 +170,18 @@ __device__ __forceinline__ void kv_values4(uint32_t w, float *x) {
   }
 }
 
-// grid (ceil(T / 64), head groups); d = D; T: type of the input rows
+// grid (ceil(T / tokens of a block), head groups); d = D; T: type of the input rows
 template <int KIND, typename T, int D>
 __global__ void __launch_bounds__(kKvThreads) k_kv_write(const KvWriteParams P) {
   constexpr int V = RopeVec<T>::kElems;      // elements of a lane
   constexpr int L = D / V;                   // lanes of a row
   constexpr int R = kKvThreads / L;          // rows of the block at a time
+  constexpr int U = 1;                       // of them in flight a thread (2 measured the same)
   __shared__ int64_t slot_sh[kKvTokens];
-  const int t0 = blockIdx.x * kKvTokens, nt = min(kKvTokens, P.T - t0);
-  if (threadIdx.x < kKvTokens) {
-    int64_t s = threadIdx.x < nt ? P.slots[t0 + threadIdx.x] : -1;
+  const int tokens = 1 << P.tok_shift;
+  const int t0 = blockIdx.x << P.tok_shift;
+  if (threadIdx.x < tokens) {
+    int64_t s = t0 + (int)threadIdx.x < P.T ? P.slots[t0 + threadIdx.x] : -1;
     if (s >= (P.g.pages << P.g.page_shift)) {
       s = -1;
       atomicOr(P.err, kDevErrRange);
@@ -136,71 +191,81 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(const KvWriteParams P) 
   __syncthreads();
   const int h0 = blockIdx.y * P.group, nh = min(P.group, P.g.heads - h0);
   const int lane = threadIdx.x % L, r0 = threadIdx.x / L;
-  const int rows = kKvTokens * nh;  // a multiple of R: whole warps take part in the row maxima
-  for (int r = r0; r < rows; r += R) {
-    const int tt = r % kKvTokens, h = h0 + r / kKvTokens;
-    const int64_t slot = slot_sh[tt];
-    uint4 raw[2];
+  const int rows = tokens * nh;
+  for (int base = 0; base < rows; base += U * R) {  // whole warps take part in the row maxima
+    int64_t row[U];
+    uint4 raw[U][2];
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-      if (slot >= 0 && P.in[w])
-        raw[w] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(P.in[w]) + (t0 + tt) * P.tok[w] +
-                                                  h * P.head[w] + lane * V);
-      else
-        raw[w] = make_uint4(0, 0, 0, 0);
-    const int64_t pg = slot >> P.g.page_shift;
-    const int64_t row = ((pg * P.g.heads + h) << P.g.page_shift) + (slot & (P.g.page - 1));
+    for (int u = 0; u < U; ++u) {
+      const int r = base + u * R + r0, tt = r & (tokens - 1), h = h0 + (r >> P.tok_shift);
+      const int64_t slot = r < rows ? slot_sh[tt] : -1;
+      row[u] = slot < 0 ? -1 : (((slot >> P.g.page_shift) * P.g.heads + h) << P.g.page_shift) + (slot & (P.g.page - 1));
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if (!P.in[w]) continue;
-      float x[V];
-      RopeVec<T>::unpack(raw[w], x);
-      if constexpr (KvCode<KIND>::kQuant) {
-        // the largest magnitude of the row, as bits: a NaN's are above an
-        // infinity's, so anything not finite is seen
-        uint32_t mb = 0;
+      for (int w = 0; w < 2; ++w) {
+        raw[u][w] = make_uint4(0, 0, 0, 0);
+        if (slot >= 0 && P.in[w])
+          raw[u][w] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(P.in[w]) + (t0 + tt) * P.tok[w] +
+                                                       h * P.head[w] + lane * V);
+      }
+    }
+    float Ms[U][2];
+    if constexpr (KvCode<KIND>::kQuant) {
+      // the scales of the rows in flight, one division for all: lane 2 u + w makes one
+      float M = 0.f;
+      int64_t at = -1;
+      int kv = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) mb = max(mb, __float_as_uint(x[i]) & 0x7fffffffu);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-        const float M = __uint_as_float(mb);
-        const bool finite = mb < 0x7f800000u;
-        uint32_t code[V / 4] = {};
-        if (finite && mb != 0) {
+        for (int w = 0; w < 2; ++w) {
+          Ms[u][w] = kv_row_max<T, L>(raw[u][w]);
+          if (lane == 2 * u + w && P.in[w]) {
+            M = Ms[u][w];
+            at = row[u];
+            kv = w;
+          }
+        }
+      if (at >= 0) P.g.scale[kv][at] = M < INFINITY ? __fdiv_rn(M, KvCode<KIND>::kTop) : __uint_as_float(0x7fc00000u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!P.in[w]) continue;
+        float x[V];
+        RopeVec<T>::unpack(raw[u][w], x);
+        if constexpr (KvCode<KIND>::kQuant) {
+          constexpr bool kExact = sizeof(T) == 4;
+          const float M = Ms[u][w];
+          uint32_t code[V / 4] = {};
           if (M > 1e-30f && M < 1e30f) {
-            const float inv = __fdiv_rn(KvCode<KIND>::kTop, M);
-#pragma unroll
-            for (int i = 0; i < V; i += 4) code[i / 4] = kv_codes4<KIND>(x + i, inv, M);
-          } else {  // c / M or c x would leave fp32: the row times 2^100 or 2^-100, which the quotient does not see
+            kv_quantise<KIND, V, kExact>(x, M, code);
+          } else if (M > 0.f && M < INFINITY) {
+            // c / M would leave fp32: the row times 2^100 or 2^-100, which the quotient does not see
             const float f = M < 1.f ? 1.2676506002282294e30f : 7.888609052210118e-31f;
             float z[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) z[i] = x[i] * f;
-            const float M2 = M * f, inv2 = __fdiv_rn(KvCode<KIND>::kTop, M2);
+            kv_quantise<KIND, V, kExact>(z, M * f, code);
+          }
+          if (row[u] >= 0) {
+            uint8_t *dst = static_cast<uint8_t *>(P.g.pool[w]) + row[u] * D + lane * V;
+            if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
+            else *reinterpret_cast<uint32_t *>(dst) = code[0];
+          }
+        } else if (row[u] >= 0) {
+          using C = typename std::conditional<KIND == kKvBf16, __nv_bfloat16, __half>::type;
+          C *dst = static_cast<C *>(P.g.pool[w]) + row[u] * D + lane * V;
+          if constexpr (V == 8) {
+            *reinterpret_cast<uint4 *>(dst) = RopeVec<C>::pack(x);
+          } else {
+            C y[4];
 #pragma unroll
-            for (int i = 0; i < V; i += 4) code[i / 4] = kv_codes4<KIND>(z + i, inv2, M2);
+            for (int i = 0; i < 4; ++i) y[i] = rope_from_float<C>(x[i]);
+            *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(y);
           }
         }
-        if (slot >= 0) {
-          uint8_t *dst = static_cast<uint8_t *>(P.g.pool[w]) + row * D + lane * V;
-          if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
-          else *reinterpret_cast<uint32_t *>(dst) = code[0];
-          if (lane == 0)
-            P.g.scale[w][row] = finite ? __fdiv_rn(M, KvCode<KIND>::kTop) : __uint_as_float(0x7fc00000u);
-        }
-      } else if (slot >= 0) {
-        using C = typename std::conditional<KIND == kKvBf16, __nv_bfloat16, __half>::type;
-        C *dst = static_cast<C *>(P.g.pool[w]) + row * D + lane * V;
-        if constexpr (V == 8) {
-          *reinterpret_cast<uint4 *>(dst) = RopeVec<C>::pack(x);
-        } else {
-          C y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = rope_from_float<C>(x[i]);
-          *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(y);
-        }
       }
-    }
   }
 }
 
@@ -216,19 +281,21 @@ __device__ __forceinline__ int kv_find_seq(const int *cu, int nseq, int t) {
   return lo;
 }
 
-// grid (ceil(T / 64), head groups); T: type of the output rows
+// grid (ceil(T / tokens of a block), head groups); T: type of the output rows
 template <int KIND, typename T, int D>
 __global__ void __launch_bounds__(kKvThreads) k_kv_read(const KvReadParams P) {
   constexpr int VO = RopeVec<T>::kElems;     // output elements of a 16-byte vector
   constexpr int V = 8;                       // elements of a lane
   constexpr int L = D / V;
   constexpr int R = kKvThreads / L;
+  constexpr int U = KvCode<KIND>::kQuant ? 4 : 2;  // rows in flight
   __shared__ int64_t slot_sh[kKvTokens];
-  const int t0 = blockIdx.x * kKvTokens, nt = min(kKvTokens, P.T - t0);
-  if (threadIdx.x < kKvTokens) {
+  const int tokens = 1 << P.tok_shift;
+  const int t0 = blockIdx.x << P.tok_shift;
+  if (threadIdx.x < tokens) {
     const int t = t0 + threadIdx.x;
     int64_t slot = -1;
-    if (threadIdx.x < nt && t >= P.cu[0] && t < P.cu[P.nseq]) {
+    if (t < P.T && t >= P.cu[0] && t < P.cu[P.nseq]) {
       const int s = kv_find_seq(P.cu, P.nseq, t);
       const int64_t p = (int64_t)(P.first ? P.first[s] : 0) + (t - P.cu[s]);
       bool ok = p >= 0 && (p >> P.g.page_shift) < P.max_pages;
@@ -244,31 +311,46 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(const KvReadParams P) {
   __syncthreads();
   const int h0 = blockIdx.y * P.group, nh = min(P.group, P.g.heads - h0);
   const int lane = threadIdx.x % L, r0 = threadIdx.x / L;
-  const int rows = kKvTokens * nh;
-#pragma unroll 2
-  for (int r = r0; r < rows; r += R) {
-    const int tt = r % kKvTokens, h = h0 + r / kKvTokens;
-    const int64_t slot = slot_sh[tt];
-    if (slot < 0) continue;
-    const int64_t row = (((slot >> P.g.page_shift) * P.g.heads + h) << P.g.page_shift) + (slot & (P.g.page - 1));
+  const int rows = tokens * nh;
+  using Raw = typename std::conditional<KvCode<KIND>::kQuant, uint2, uint4>::type;
+  for (int base = 0; base < rows; base += U * R) {
+    Raw raw[U][2];
+    float sc[U][2];
+    bool have[U];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if (!P.out[w]) continue;
-      float x[V];
-      if constexpr (KvCode<KIND>::kQuant) {
-        const uint2 c = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(P.g.pool[w]) + row * D + lane * V);
-        const float s = P.g.scale[w][row];
-        kv_values4<KIND>(c.x, x);
-        kv_values4<KIND>(c.y, x + 4);
+    for (int u = 0; u < U; ++u) {
+      const int r = base + u * R + r0, tt = r & (tokens - 1), h = h0 + (r >> P.tok_shift);
+      const int64_t slot = r < rows ? slot_sh[tt] : -1;
+      have[u] = slot >= 0;
+      const int64_t row = (((slot >> P.g.page_shift) * P.g.heads + h) << P.g.page_shift) + (slot & (P.g.page - 1));
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] *= s;
-      } else {
-        using C = typename std::conditional<KIND == kKvBf16, __nv_bfloat16, __half>::type;
-        RopeVec<C>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const C *>(P.g.pool[w]) + row * D + lane * V), x);
+      for (int w = 0; w < 2; ++w)
+        if (have[u] && P.out[w]) {
+          raw[u][w] = *reinterpret_cast<const Raw *>(static_cast<const uint8_t *>(P.g.pool[w]) +
+                                                     (row * D + lane * V) * KvCode<KIND>::kBytes);
+          if constexpr (KvCode<KIND>::kQuant) sc[u][w] = P.g.scale[w][row];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = base + u * R + r0, tt = r & (tokens - 1), h = h0 + (r >> P.tok_shift);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        if (!have[u] || !P.out[w]) continue;
+        float x[V];
+        if constexpr (KvCode<KIND>::kQuant) {
+          kv_values4<KIND>(raw[u][w].x, x);
+          kv_values4<KIND>(raw[u][w].y, x + 4);
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] *= sc[u][w];
+        } else {
+          using C = typename std::conditional<KIND == kKvBf16, __nv_bfloat16, __half>::type;
+          RopeVec<C>::unpack(raw[u][w], x);
+        }
+        T *dst = static_cast<T *>(P.out[w]) + (t0 + tt) * P.tok[w] + h * P.head[w] + lane * V;
+#pragma unroll
+        for (int i = 0; i < V; i += VO) *reinterpret_cast<uint4 *>(dst + i) = RopeVec<T>::pack(x + i);
       }
-      T *dst = static_cast<T *>(P.out[w]) + (t0 + tt) * P.tok[w] + h * P.head[w] + lane * V;
-#pragma unroll
-      for (int i = 0; i < V; i += VO) *reinterpret_cast<uint4 *>(dst + i) = RopeVec<T>::pack(x + i);
     }
   }
 }

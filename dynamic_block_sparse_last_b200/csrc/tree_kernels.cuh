@@ -295,15 +295,17 @@ template <int KIND, int D, int MT>
 struct TreeCfg {
   static constexpr bool kQuant = KvCode<KIND>::kQuant;
   static constexpr int BM = 16 * MT;
-  // 16 rows: two CTAs per SM of four warps, 200 registers a thread; 32 rows: one of
-  // eight.  Over a quantised cache a warp takes 32 tokens at a time: its work per
-  // byte is larger, and two independent halves hide each other's latency.
-  static constexpr int kWarps = MT == 1 ? 4 : 8;
-  static constexpr int kCtas = MT == 1 ? 2 : 1;
-  static constexpr int kThreads = (MT == 1 ? kWarps + 1 : kWarps + 4) * 32;  // the producer; 32 rows: in a warpgroup of its own
-  // Registers of 32 rows: the block starts with 168 a thread (384 threads), and 2 x 128 x 216 + 128 x 56 = 62464 <= 384 x 168.
+  // Two CTAs per SM of four warps, up to 200 registers a thread; 32 rows of 128-wide
+  // heads, whose O alone is 128 registers: one of eight warps.  Where there is room a
+  // warp takes 32 tokens at a time (quantised caches, where its work per byte is
+  // larger, and 64-wide heads): two independent halves hide each other's latency.
+  static constexpr bool kBig = MT == 2 && D == 128;
+  static constexpr int kWarps = kBig ? 8 : 4;
+  static constexpr int kCtas = kBig ? 1 : 2;
+  static constexpr int kThreads = (kBig ? kWarps + 4 : kWarps + 1) * 32;  // the producer; kBig: in a warpgroup of its own
+  // Registers when kBig: the block starts with 168 a thread (384 threads), and 2 x 128 x 216 + 128 x 56 = 62464 <= 384 x 168.
   static constexpr int kRegs = 216, kRegsTma = 56;
-  static constexpr int TOK = kQuant && MT == 1 ? 32 : 16;  // tokens of a warp in a tile
+  static constexpr int TOK = (kQuant && MT == 1) || D == 64 ? 32 : 16;  // tokens of a warp in a tile
   static constexpr int BN = kWarps * TOK;                 // tokens of a tile
   static constexpr int RB = D * KvCode<KIND>::kBytes;     // bytes of a cached row
   static constexpr int kBoxB = RB < 128 ? RB : 128;       // bytes of a box row
@@ -315,7 +317,7 @@ struct TreeCfg {
   static constexpr int kStage = 2 * kTile;
   static constexpr int kStageAll = kStage + (kQuant ? 2 * BN * 4 : 0);  // with the scales
   // as many as leave room for Q, obuf and the other CTA (227 KB an SM), 6 at most
-  static constexpr int kFit = (MT == 1 ? 99000 : 200000) / kStageAll, kStages = kFit > 6 ? 6 : kFit;
+  static constexpr int kFit = (kBig ? 200000 : 99000) / kStageAll, kStages = kFit > 6 ? 6 : kFit;
   static constexpr int kScaleOff = kStages * kStage;      // [stage][K, V][BN] fp32
   static constexpr int kQOff = kScaleOff + (kQuant ? kStages * 2 * BN * 4 : 0);  // [MT][steps][32] uint4
   static constexpr int kLd = D + 4;                       // row pitch of obuf (fp32)
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
 
   if (warp >= C::kWarps) {
     // ------------------------------------------------------------ producer
-    if constexpr (MT > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsTma));
+    if constexpr (C::kBig) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsTma));
     if (warp > C::kWarps) return;
     // A tile is BN / min(page, 64) pieces, each of one page; lane i moves piece i.
     const int piece = min(P.page, 64), pieces = C::BN / piece;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
   }
 
   // -------------------------------------------------------------- consumers
-  if constexpr (MT > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs));
+  if constexpr (C::kBig) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegs));
   const int q4 = lane >> 2, c4 = lane & 3;
   const uint32_t qbase = base + C::kQOff;
   float *obuf = reinterpret_cast<float *>(smem_raw + (base - smem_u32(smem_raw)) + C::kOOff);
@@ -570,8 +572,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
           }
         }
         // ---- scales and masks; a thread has tokens 8i + 2c, 8i + 2c + 1 of rows q, q + 8
-        float vs[2 * NT];
-        const uint32_t sc = base + C::kScaleOff + st * 2 * C::BN * 4 + (key0 + 2 * c4) * 4;
+        [[maybe_unused]] float vs[2 * NT];
+        [[maybe_unused]] const uint32_t sc = base + C::kScaleOff + st * 2 * C::BN * 4 + (key0 + 2 * c4) * 4;
         if constexpr (C::kQuant) {
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
             mxl[mt][hh] = mx;
             ask |= mx > m[mt][hh] + C::kSlack;
           }
-        float vmx = 0.f;
+        [[maybe_unused]] float vmx = 0.f;
         if constexpr (C::kQuant) {
 #pragma unroll
           for (int k = 0; k < 2 * NT; ++k) vmx = fmaxf(vmx, vs[k]);

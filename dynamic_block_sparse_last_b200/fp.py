@@ -386,29 +386,41 @@ def _refuse(where, why):
     raise FpError(FP_ERR_ARG, f"{where}: {why}")
 
 
-def _on(where, device, *tensors):
-    """Every tensor is on `device`, and that is the current device: its stream is the one used."""
-    if device.type != "cuda":
+# The checks below run before every call of a few microseconds, so they are few
+# and read each property of a tensor once.
+
+def _here(where, t):
+    """The device of t, which must be the current one: its stream is the one used."""
+    dev = t.get_device()
+    if dev < 0:
         _refuse(where, "tensors must be on a CUDA device")
-    for t in tensors:
-        if t is not None and t.device != device:
-            _refuse(where, f"tensors on {t.device} and {device}")
-    if torch.cuda.current_device() != device.index:
-        _refuse(where, f"tensors on {device}, which is not the current device")
+    if dev != torch.cuda.current_device():
+        _refuse(where, f"tensors on cuda:{dev}, which is not the current device")
+    return dev
 
 
-def _table(where, name, t, dtype, *shape):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        _refuse(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+def _raw_stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _tokens(where, name, t, dtype, *shape):
-    if t.dtype != dtype or t.shape != shape or t.stride(2) != 1:
-        _refuse(where, f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous elements")
+def _table(where, name, t, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(where, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}")
+    return t.data_ptr()
 
 
-def _rows(t):
-    return (None, 0, 0) if t is None else (t.data_ptr(), t.stride(1), t.stride(0))
+def _tokens(where, name, t, dtype, shape, dev):
+    """Address, token stride and head stride of a [heads, tokens, d] tensor."""
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or st[2] != 1 or t.get_device() != dev:
+        _refuse(where, f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous elements on cuda:{dev}")
+    return t.data_ptr(), st[1], st[0]
+
+
+_NONE = (None, 0, 0)
 
 
 class Rope:
@@ -436,22 +448,24 @@ class Rope:
         """Rotates q_in [Hq, T, d] and k_in [Hkv, T, d] (either may be None, with its
         output) by the positions pos (int32 [T]) into q_out, k_out (which may be the
         inputs); inverse: the transpose, the gradient of the inputs."""
-        where, any_in = "fp_rope_apply", q_in if q_in is not None else k_in
-        if any_in is None:
-            _refuse(where, "neither q nor k")
-        T, d = any_in.shape[1:] if any_in.dim() == 3 else (0, 0)
-        _on(where, any_in.device, q_in, k_in, q_out, k_out, pos)
-        for name, x, y in (("q", q_in, q_out), ("k", k_in, k_out)):
-            if (x is None) != (y is None):
-                _refuse(where, f"{name}_in and {name}_out go together")
-            if x is not None:
-                _tokens(where, name + "_in", x, any_in.dtype, x.shape[0], T, self.d)
-                _tokens(where, name + "_out", y, any_in.dtype, x.shape[0], T, self.d)
-        _table(where, "pos", pos, torch.int32, T)
-        _check(_lib.fp_rope_apply(self.handle, *_rows(q_in), *_rows(k_in), *_rows(q_out), *_rows(k_out),
-                                  _DTYPES.get(any_in.dtype, -1), T, 0 if q_in is None else q_in.shape[0],
-                                  0 if k_in is None else k_in.shape[0], pos.data_ptr(), int(inverse), _stream(stream)),
-               where)
+        where, x = "fp_rope_apply", q_in if q_in is not None else k_in
+        if x is None or x.dim() != 3:
+            _refuse(where, "q or k must be given, as [heads, tokens, d]")
+        if (q_in is None) != (q_out is None) or (k_in is None) != (k_out is None):
+            _refuse(where, "an input and its output go together")
+        dev, T, dt = _here(where, x), x.shape[1], x.dtype
+        hq = hkv = 0
+        qi = qo = ki = ko = _NONE
+        if q_in is not None:
+            hq = q_in.shape[0]
+            shape = (hq, T, self.d)
+            qi, qo = _tokens(where, "q_in", q_in, dt, shape, dev), _tokens(where, "q_out", q_out, dt, shape, dev)
+        if k_in is not None:
+            hkv = k_in.shape[0]
+            shape = (hkv, T, self.d)
+            ki, ko = _tokens(where, "k_in", k_in, dt, shape, dev), _tokens(where, "k_out", k_out, dt, shape, dev)
+        _check(_lib.fp_rope_apply(self.handle, *qi, *ki, *qo, *ko, _DTYPES.get(dt, -1), T, hq, hkv,
+                                  _table(where, "pos", pos, torch.int32, (T,), dev), inverse, _raw_stream(stream, dev)), where)
 
     def free(self):
         if self.handle:
@@ -476,32 +490,28 @@ class KvCache:
         if k_pool.dim() != 4:
             _refuse(where, "pools are [pages, Hkv, page, d]")
         pages, self.Hkv, self.page, self.d = k_pool.shape
-        _on(where, k_pool.device, k_pool, v_pool, k_scale, v_scale)
-        for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-            _table(where, name, t, k_pool.dtype, *k_pool.shape)
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is not None:
-                _table(where, name, t, torch.float32, *k_pool.shape[:3])
-        self.pools, self.pages, self.device = (k_pool, v_pool, k_scale, v_scale), pages, k_pool.device
+        dev = _here(where, k_pool)
+        ptr = [_table(where, n, t, k_pool.dtype, k_pool.shape, dev) for n, t in (("k_pool", k_pool), ("v_pool", v_pool))]
+        ptr += [t if t is None else _table(where, n, t, torch.float32, k_pool.shape[:3], dev)
+                for n, t in (("k_scale", k_scale), ("v_scale", v_scale))]
+        self.pools, self.pages, self.device = (k_pool, v_pool, k_scale, v_scale), pages, dev
         h = ctypes.c_void_p()
-        _check(_lib.fp_kv_create(_ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
-                                 _DTYPES.get(k_pool.dtype, -1), pages, self.page, self.Hkv, self.d, ctypes.byref(h)), where)
+        _check(_lib.fp_kv_create(*ptr, _DTYPES.get(k_pool.dtype, -1), pages, self.page, self.Hkv, self.d, ctypes.byref(h)),
+               where)
         self.handle = h.value
 
     def write(self, k, v, slots, stream=None):
         """Writes the tokens k, v [Hkv, T, d] (either may be None) to slots (int64 [T],
         page * page_size + offset; negative: skipped), quantising each row."""
         where, x = "fp_kv_write", k if k is not None else v
-        if x is None:
-            _refuse(where, "neither k nor v")
-        _on(where, self.device, k, v, slots)
-        T = x.shape[1] if x.dim() == 3 else 0
-        for name, t in (("k", k), ("v", v)):
-            if t is not None:
-                _tokens(where, name, t, x.dtype, self.Hkv, T, self.d)
-        _table(where, "slots", slots, torch.int64, T)
-        _check(_lib.fp_kv_write(self.handle, *_rows(k), *_rows(v), _DTYPES.get(x.dtype, -1), T, slots.data_ptr(),
-                                _stream(stream)), where)
+        if x is None or x.dim() != 3:
+            _refuse(where, "k or v must be given, as [heads, tokens, d]")
+        dev, T, dt = self.device, x.shape[1], x.dtype
+        shape = (self.Hkv, T, self.d)
+        kk = _NONE if k is None else _tokens(where, "k", k, dt, shape, dev)
+        vv = _NONE if v is None else _tokens(where, "v", v, dt, shape, dev)
+        _check(_lib.fp_kv_write(self.handle, *kk, *vv, _DTYPES.get(dt, -1), T,
+                                _table(where, "slots", slots, torch.int64, (T,), dev), _raw_stream(stream, dev)), where)
 
     def read(self, block_table, cu_seqlens, k, v, first=None, stream=None):
         """Reads cached tokens into k, v [Hkv, T, d] (either may be None): rows
@@ -509,22 +519,17 @@ class KvCache:
         of sequence s.  block_table int32 [nseq, max_pages], cu_seqlens int32
         [nseq + 1], first int32 [nseq], on the device."""
         where, x = "fp_kv_read", k if k is not None else v
-        if x is None:
-            _refuse(where, "neither k nor v")
-        _on(where, self.device, k, v, block_table, cu_seqlens, first)
-        T = x.shape[1] if x.dim() == 3 else 0
-        for name, t in (("k", k), ("v", v)):
-            if t is not None:
-                _tokens(where, name, t, x.dtype, self.Hkv, T, self.d)
-        if block_table.dim() != 2:
-            _refuse(where, "block_table is [nseq, max_pages]")
+        if x is None or x.dim() != 3 or block_table.dim() != 2:
+            _refuse(where, "k or v must be given, as [heads, tokens, d], and block_table is [nseq, max_pages]")
+        dev, T, dt = self.device, x.shape[1], x.dtype
+        shape = (self.Hkv, T, self.d)
+        kk = _NONE if k is None else _tokens(where, "k", k, dt, shape, dev)
+        vv = _NONE if v is None else _tokens(where, "v", v, dt, shape, dev)
         nseq, width = block_table.shape
-        _table(where, "block_table", block_table, torch.int32, nseq, width)
-        _table(where, "cu_seqlens", cu_seqlens, torch.int32, nseq + 1)
-        if first is not None:
-            _table(where, "first", first, torch.int32, nseq)
-        _check(_lib.fp_kv_read(self.handle, block_table.data_ptr(), width, cu_seqlens.data_ptr(), _ptr(first), nseq, T,
-                               *_rows(k), *_rows(v), _DTYPES.get(x.dtype, -1), _stream(stream)), where)
+        _check(_lib.fp_kv_read(self.handle, _table(where, "block_table", block_table, torch.int32, (nseq, width), dev), width,
+                               _table(where, "cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), dev),
+                               first if first is None else _table(where, "first", first, torch.int32, (nseq,), dev),
+                               nseq, T, *kk, *vv, _DTYPES.get(dt, -1), _raw_stream(stream, dev)), where)
 
     def free(self):
         if self.handle:
@@ -555,20 +560,17 @@ def fp_tree_attn(q, kv: KvCache, block_table, kv_len, cu_q, max_q, mask, scale, 
     where = "fp_tree_attn"
     if q.dim() != 3 or block_table.dim() != 2:
         _refuse(where, "q is [Hq, T, d], block_table [nseq, max_pages]")
-    Hq, T, d = q.shape
+    dev, dt = kv.device, q.dtype
+    Hq, T, _ = q.shape
     nseq, width = block_table.shape
-    _on(where, kv.device, q, block_table, kv_len, cu_q, mask, out, work, lse)
-    _tokens(where, "q", q, q.dtype, Hq, T, kv.d)
-    _tokens(where, "out", out, q.dtype, Hq, T, kv.d)
-    _table(where, "block_table", block_table, torch.int32, nseq, width)
-    _table(where, "kv_len", kv_len, torch.int32, nseq)
-    _table(where, "cu_q", cu_q, torch.int32, nseq + 1)
-    if mask is not None:
-        _table(where, "mask", mask, torch.int64, T, (max_q + 63) // 64)
-    if lse is not None:
-        _table(where, "lse", lse, torch.float32, Hq, T)
-    if not work.is_contiguous():
-        _refuse(where, "work must be contiguous")
-    _check(_lib.fp_tree_attn(kv.handle, *_rows(q), _DTYPES.get(q.dtype, -1), T, Hq, block_table.data_ptr(), width,
-                             kv_len.data_ptr(), cu_q.data_ptr(), nseq, max_q, _ptr(mask), scale, *_rows(out), _ptr(lse),
-                             work.data_ptr(), work.numel() * work.element_size(), _stream(stream)), where)
+    shape = (Hq, T, kv.d)
+    if not work.is_contiguous() or work.get_device() != dev:
+        _refuse(where, f"work must be contiguous, on cuda:{dev}")
+    _check(_lib.fp_tree_attn(kv.handle, *_tokens(where, "q", q, dt, shape, dev), _DTYPES.get(dt, -1), T, Hq,
+                             _table(where, "block_table", block_table, torch.int32, (nseq, width), dev), width,
+                             _table(where, "kv_len", kv_len, torch.int32, (nseq,), dev),
+                             _table(where, "cu_q", cu_q, torch.int32, (nseq + 1,), dev), nseq, max_q,
+                             mask if mask is None else _table(where, "mask", mask, torch.int64, (T, (max_q + 63) // 64), dev),
+                             scale, *_tokens(where, "out", out, dt, shape, dev),
+                             lse if lse is None else _table(where, "lse", lse, torch.float32, (Hq, T), dev),
+                             work.data_ptr(), work.nbytes, _raw_stream(stream, dev)), where)

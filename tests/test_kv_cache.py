@@ -119,6 +119,40 @@ def test_every_quotient_near_a_border(fp, kind):
         assert torch.equal(raw(p[0])[0, 0, :T].view(dt).float(), code[:, 0]), M
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_ratio_of_16_bit_mantissas(fp, kind, dtype):
+    """All mantissas b over those of M (all of bf16's 128, 48 of fp16's 1024, the ones with the most borders
+    among them), over the binades that reach a code other than 0: exact ties and all that is near one."""
+    bits = {"bf16": 8, "f16": 11}[dtype]
+    one = 1 << (bits - 1)
+    tops = range(one, 2 * one)
+    if dtype == "f16":
+        tops = sorted({one, 2 * one - 1, 127 * 8 + 0, 127 * 16 - one, 254 * 8 // 2} | set(range(one, 2 * one, 23)))
+        tops = [t for t in tops if one <= t < 2 * one]
+    b = torch.arange(one, 2 * one, dtype=torch.float64)
+    binades = range(0, 10 if kind == "int8" else 20)
+    x = torch.cat([b * 2.0 ** -(k + bits - 1) for k in binades])     # below 2
+    if dtype == "f16":
+        x = x.half().double().unique()                              # fp16's subnormals repeat
+    rows = []
+    for a in tops:
+        M = a / one
+        y = x[x <= M]
+        y = torch.cat([y, torch.zeros(-len(y) % 127)]).view(-1, 127)
+        rows.append(torch.cat([torch.full((len(y), 1), M, dtype=torch.float64), y], 1))
+    k = torch.cat(rows).to(TYPES[dtype])
+    assert torch.equal(k.double(), torch.cat(rows))                 # the rows are what they are meant to be
+    k = k.cuda()
+    k[::2, 1:] *= -1
+    T, page = len(k), 128
+    pages = -(-T // page)
+    p = pools(kind, pages, 1, page, 128)
+    fp.KvCache(*p).write(k[None], None, torch.arange(T, device="cuda"))
+    code, _ = codes_of(k, kind, True)
+    assert torch.equal(raw(p[0]).view(-1, 128)[:T].view(CODES[kind][0]).float(), code)
+
+
 def test_extreme_and_non_finite_rows(fp):
     d, page = 128, 16
     p = pools("int8", 1, 1, page, d)
