@@ -423,8 +423,8 @@ bool allow_smem(K kernel, int bytes, std::atomic<void *> (&where)[128]) {
 template <int D>
 int launch_join(const TreeParams &P, int bm, int ctas, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (bm + 7) / 8);
-  cfg.blockDim = dim3(8 * D / 4);
+  cfg.gridDim = dim3(ctas, (bm + 1024 / D - 1) / (1024 / D));
+  cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

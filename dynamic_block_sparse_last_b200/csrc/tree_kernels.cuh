@@ -450,16 +450,17 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
     // Q fragments: a warp takes a row, a lane 4 neighbouring elements, which are one
     // thread's (a0, a2) or (a1, a3) of one step; a warp's rows are under way at once
     constexpr int RW = C::BM / C::kWarps;
+    long long off = -1;  // of row warp + lane * kWarps
+    if (lane < RW && warp + lane * C::kWarps < R) {
+      const int gr = rbase + warp + lane * C::kWarps, i = gr / P.g;
+      off = (w.q.row0 + i) * P.q_tok + (w.j * P.g + gr - i * P.g) * P.q_head;
+    }
     uint2 qx[RW];
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
-      const int r = warp + k * C::kWarps;
+      const long long o = __shfl_sync(0xffffffffu, off, k);
       qx[k] = make_uint2(0u, 0u);
-      if (r < R && lane < D / 4) {
-        const int i = (rbase + r) / P.g, h = w.j * P.g + (rbase + r) - i * P.g;
-        qx[k] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(P.q) + (w.q.row0 + i) * P.q_tok +
-                                                 h * P.q_head + 4 * lane);
-      }
+      if (o >= 0 && lane < D / 4) qx[k] = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(P.q) + o + 4 * lane);
     }
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
@@ -792,30 +793,32 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
           fin_l[r] = L;
         }
       }
+    // O in kWarps parts; in step k a warp adds its values of part (warp + k) mod kWarps:
+    // no two warps at the same part, and each part's sum in a fixed order
     for (int k = 0; k < C::kWarps; ++k) {
-      if (warp == k) {
+      const int mine = (warp + k) & (C::kWarps - 1);
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int hh = 0; hh < 2; ++hh) {
-            float *row = obuf + (16 * mt + 8 * hh + q4) * C::kLd;
+        for (int x = 0; x < C::kBoxes; ++x)
 #pragma unroll
-            for (int x = 0; x < C::kBoxes; ++x)
+          for (int i = 0; i < C::VE; i += 4)
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e) {
+              const int quarter = D == 128 ? (C::VE * x + i) / 4 : (i / 4) * 2 + e;  // of a row's columns
+              if (mine != (C::kBig ? mt * 4 + quarter : quarter)) continue;
 #pragma unroll
-                for (int i = 0; i < C::VE; i += 4) {
-                  float4 *dst = reinterpret_cast<float4 *>(row + 64 * x + C::VE * (2 * c4 + e) + i);
-                  float4 v = k == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *dst;
-                  const int oi = C::VE * x + i, oe = 2 * hh + e;
-                  v.x = fmaf(o[mt][oi][oe], f[mt][hh], v.x);
-                  v.y = fmaf(o[mt][oi + 1][oe], f[mt][hh], v.y);
-                  v.z = fmaf(o[mt][oi + 2][oe], f[mt][hh], v.z);
-                  v.w = fmaf(o[mt][oi + 3][oe], f[mt][hh], v.w);
-                  *dst = v;
-                }
-          }
-      }
+              for (int hh = 0; hh < 2; ++hh) {
+                float4 *dst = reinterpret_cast<float4 *>(obuf + (16 * mt + 8 * hh + q4) * C::kLd + 64 * x + C::VE * (2 * c4 + e) + i);
+                float4 v = k == 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *dst;
+                const int oi = C::VE * x + i, oe = 2 * hh + e;
+                v.x = fmaf(o[mt][oi][oe], f[mt][hh], v.x);
+                v.y = fmaf(o[mt][oi + 1][oe], f[mt][hh], v.y);
+                v.z = fmaf(o[mt][oi + 2][oe], f[mt][hh], v.z);
+                v.w = fmaf(o[mt][oi + 3][oe], f[mt][hh], v.w);
+                *dst = v;
+              }
+            }
       named_sync(1, NC);
     }
     // ---- out, or this CTA's part of it
@@ -871,48 +874,56 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
 }
 
 // Adds up the parts of the units that several CTAs share, in the order of the
-// CTAs.  grid (C, row groups of 8), a thread per 4 columns.
+// CTAs.  grid (C, row groups), a warp per row (D = 64: two rows), a lane per 4
+// columns.  A latency, not a bandwidth: so the first 16 parts are under way before
+// their weights 2^(m - M) are known, which the lanes work out a part each.
 template <int D>
-__global__ void __launch_bounds__(8 * D / 4) k_tree_join(const __grid_constant__ TreeParams P, int BM) {
+__global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeParams P, int BM) {
+  constexpr int G = D / 4, RPB = 256 / G, NP = 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeDesc d = P.desc[blockIdx.x];
   if (d.n == 0) return;
   const int R = min(BM, d.n * P.g - d.row_tile0);
-  const int r = blockIdx.y * 8 + threadIdx.x / (D / 4), col = 4 * (threadIdx.x % (D / 4));
+  const int r = blockIdx.y * RPB + threadIdx.x / G, gl = threadIdx.x % G, col = 4 * gl;
   if (r >= R) return;
-  // The lanes of a row (D / 4 of them) take a part each for the weights, 2^(m - M)
-  // of part c, then walk the parts together, the weights coming from their lanes.
-  constexpr int G = D / 4;
-  const int c0 = blockIdx.x, parts = d.last - c0 + 1, gl = threadIdx.x % G;
+  const int c0 = blockIdx.x, parts = d.last - c0 + 1;
   const unsigned gm = G == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
+  auto row_of = [&](int k) { return (int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * BM + r; };
   auto ml_of = [&](int k) {
-    if (k >= parts) return make_float2(-INFINITY, 0.f);
-    return *reinterpret_cast<const float2 *>(P.part_ml + ((int64_t)(2 * (c0 + k) + (k == 0 ? 1 : 0)) * BM + r) * 2);
+    return k < parts ? *reinterpret_cast<const float2 *>(P.part_ml + row_of(k) * 2) : make_float2(-INFINITY, 0.f);
   };
-  float M = -INFINITY;
-  for (int k = gl; k < parts; k += G) M = fmaxf(M, ml_of(k).x);
+  float4 v[NP];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+      v[k] = k0 + k < parts ? *reinterpret_cast<const float4 *>(P.part + row_of(k0 + k) * D + col) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  load(0);
+  const float2 first = ml_of(gl);
+  float M = first.x;
+  for (int k = gl + G; k < parts; k += G) M = fmaxf(M, ml_of(k).x);
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(gm, M, o));
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < parts; k0 += G) {
-    const float2 ml = ml_of(k0 + gl);
+    const float2 ml = k0 == 0 ? first : ml_of(k0 + gl);
     const float f = ex2(ml.x - ref);
     float lsum = ml.y * f;
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) lsum += __shfl_xor_sync(gm, lsum, o);
     L += lsum;
-    const int n = min(G, parts - k0);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const int64_t at = (int64_t)(2 * (c0 + k0 + k) + (k0 + k == 0 ? 1 : 0)) * BM + r;
-      const float4 v = *reinterpret_cast<const float4 *>(P.part + at * D + col);
-      const float fk = __shfl_sync(gm, f, k, G);
-      acc.x = fmaf(v.x, fk, acc.x);
-      acc.y = fmaf(v.y, fk, acc.y);
-      acc.z = fmaf(v.z, fk, acc.z);
-      acc.w = fmaf(v.w, fk, acc.w);
+    for (int kk = 0; kk < G && k0 + kk < parts; kk += NP) {
+      if (k0 + kk > 0) load(k0 + kk);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const float fk = __shfl_sync(gm, f, kk + k, G);  // 0 behind the last part
+        acc.x = fmaf(v[k].x, fk, acc.x);
+        acc.y = fmaf(v[k].y, fk, acc.y);
+        acc.z = fmaf(v[k].z, fk, acc.z);
+        acc.w = fmaf(v[k].w, fk, acc.w);
+      }
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
