@@ -51,10 +51,13 @@ struct TcCfg {
   static constexpr int kBoxB = RB < 128 ? RB : 128;
   static constexpr int kRaw = 128 * RB;                   // bytes of a raw K (or V) tile
   static constexpr int kRow16 = RB / 16;                  // 16-byte pieces of a row
-  static constexpr int kStages = kQuant ? (PAIR && D == 128 ? 2 : 3) : (D == 128 ? 2 : 3);  // raw tiles in flight
-  static constexpr int kOps = kQuant ? 1 : kStages;       // operand buffers: the raw tiles themselves when not quantised
-  static constexpr int kQOff = 0, kKOff = (PAIR ? 2 : 1) * kOp, kVOff = kKOff + kOps * kOp;
-  static constexpr int kRkOff = kQuant ? kVOff + kOps * kOp : kKOff, kRvOff = kQuant ? kRkOff + kStages * kRaw : kVOff;
+  static constexpr int kStages = D == 128 ? 2 : 3;        // raw tiles in flight
+  // Operand buffers: the raw tiles themselves when not quantised; else one, two where
+  // they fit (V first: its conversion would wait for the product before it).
+  static constexpr int kOpsK = !kQuant ? kStages : D == 64 ? 2 : 1;
+  static constexpr int kOpsV = !kQuant ? kStages : D == 64 || !PAIR ? 2 : 1;
+  static constexpr int kQOff = 0, kKOff = (PAIR ? 2 : 1) * kOp, kVOff = kKOff + kOpsK * kOp;
+  static constexpr int kRkOff = kQuant ? kVOff + kOpsV * kOp : kKOff, kRvOff = kQuant ? kRkOff + kStages * kRaw : kVOff;
   static constexpr int kEnd = kRvOff + kStages * kRaw;
   static constexpr int kRsOff = kEnd;                     // raw scales [stage][K, V][128] fp32
   static constexpr int kSmem = kRsOff + (kQuant ? kStages * 1024 : 0) + 1024;
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int kQWarps = PAIR ? 4 : 8;   // warps that write a query tile
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_q[2], bar_rkf[C::kStages], bar_rke[C::kStages], bar_rvf[C::kStages],
-      bar_rve[C::kStages], bar_kfull[C::kOps], bar_kempty[C::kOps], bar_vfull[C::kOps], bar_vempty[C::kOps], bar_sfull[2],
+      bar_rve[C::kStages], bar_kfull[C::kOpsK], bar_kempty[C::kOpsK], bar_vfull[C::kOpsV], bar_vempty[C::kOpsV], bar_sfull[2],
       bar_pfull[2], bar_odone[2], bar_scfull[C::kSc], bar_scempty[C::kSc];
   __shared__ __align__(16) float sc_k[C::kSc][kTcBN], sc_v[C::kSc][kTcBN];
   __shared__ int sc_exp[C::kSc];
@@ -266,9 +269,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_u32(&bar_rvf[i]), 1);
       mbar_init(smem_u32(&bar_rve[i]), 4);
     }
-    for (int i = 0; i < C::kOps; ++i) {
+    for (int i = 0; i < C::kOpsK; ++i) {
       mbar_init(smem_u32(&bar_kfull[i]), 4);
       mbar_init(smem_u32(&bar_kempty[i]), 1);
+    }
+    for (int i = 0; i < C::kOpsV; ++i) {
       mbar_init(smem_u32(&bar_vfull[i]), 4);
       mbar_init(smem_u32(&bar_vempty[i]), 1);
     }
@@ -312,8 +317,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < I + 2 && ok; ++i) {
           const int t = i & 1;
           if (i >= 2) {
-            const int u = u0 + (PAIR ? (i - 2) >> 1 : i - 2), st = u % C::kOps;
-            if ((!PAIR || t == 0) && !mbar_wait(smem_u32(&bar_vfull[st]), (u / C::kOps) & 1, abort_flag, P.err)) { ok = false; break; }
+            const int u = u0 + (PAIR ? (i - 2) >> 1 : i - 2), st = u % C::kOpsV;
+            if ((!PAIR || t == 0) && !mbar_wait(smem_u32(&bar_vfull[st]), (u / C::kOpsV) & 1, abort_flag, P.err)) { ok = false; break; }
             if (!mbar_wait(smem_u32(&bar_pfull[t]), npv[t] & 1, abort_flag, P.err)) { ok = false; break; }
             tc_fence_after();
             const uint32_t dv = dv_lo + ((st * C::kOp) >> 4);
@@ -326,10 +331,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (!PAIR || t == 1) tc_commit(smem_u32(&bar_vempty[st]));
           }
           if (i < I) {
-            const int u = u0 + (PAIR ? i >> 1 : i), st = u % C::kOps;
+            const int u = u0 + (PAIR ? i >> 1 : i), st = u % C::kOpsK;
             // K of an unquantised cache is used as TMA left it
             const uint32_t full = C::kQuant ? smem_u32(&bar_kfull[st]) : smem_u32(&bar_rkf[st]);
-            if ((!PAIR || t == 0) && !mbar_wait(full, (u / C::kOps) & 1, abort_flag, P.err)) { ok = false; break; }
+            if ((!PAIR || t == 0) && !mbar_wait(full, (u / C::kOpsK) & 1, abort_flag, P.err)) { ok = false; break; }
             tc_fence_after();
             const uint32_t dq = dq_lo + (((PAIR ? t : 0) * C::kOp) >> 4), dk = dk_lo + ((st * C::kOp) >> 4);
 #pragma unroll
@@ -412,8 +417,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (; more && ok; more = w.next(P, C::BM, kTcBN)) {
       kexp = -126;
       for (int t = w.a; t < w.b; ++t, ++u) {
-        const int rst = u % C::kStages, st = u % C::kOps;
-        const uint32_t rph = (u / C::kStages) & 1, oph = ((u / C::kOps) - 1) & 1;
+        const int rst = u % C::kStages, kst = u % C::kOpsK, vst = u % C::kOpsV;
+        const uint32_t rph = (u / C::kStages) & 1, kph = ((u / C::kOpsK) - 1) & 1, vph = ((u / C::kOpsV) - 1) & 1;
         const int left = w.q.len - t * kTcBN, fresh = left - w.q.n;  // tokens to the end; before the first new one
         if constexpr (C::kQuant) {
           ok = mbar_wait(smem_u32(&bar_rkf[rst]), rph, abort_flag, P.err);
@@ -447,25 +452,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar_scfull[ss]));
           }
-          if (ok && u >= C::kOps) ok = mbar_wait(smem_u32(&bar_kempty[st]), oph, abort_flag, P.err);
+          if (ok && u >= C::kOpsK) ok = mbar_wait(smem_u32(&bar_kempty[kst]), kph, abort_flag, P.err);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          tc_convert<C, KIND, false>(base + C::kRkOff + rst * C::kRaw, sk + st * C::kOp, ct, 0, 0, bad);
+          tc_convert<C, KIND, false>(base + C::kRkOff + rst * C::kRaw, sk + kst * C::kOp, ct, 0, 0, bad);
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_u32(&bar_kfull[st]));
+            mbar_arrive(smem_u32(&bar_kfull[kst]));
             mbar_arrive(smem_u32(&bar_rke[rst]));
           }
           ok = mbar_wait(smem_u32(&bar_rvf[rst]), rph, abort_flag, P.err);
-          if (ok && u >= C::kOps) ok = mbar_wait(smem_u32(&bar_vempty[st]), oph, abort_flag, P.err);
+          if (ok && u >= C::kOpsV) ok = mbar_wait(smem_u32(&bar_vempty[vst]), vph, abort_flag, P.err);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          if (fresh < kTcBN) tc_convert<C, KIND, true>(base + C::kRvOff + rst * C::kRaw, sv + st * C::kOp, ct, fresh, left, bad);
-          else tc_convert<C, KIND, false>(base + C::kRvOff + rst * C::kRaw, sv + st * C::kOp, ct, 0, 0, bad);
+          if (fresh < kTcBN) tc_convert<C, KIND, true>(base + C::kRvOff + rst * C::kRaw, sv + vst * C::kOp, ct, fresh, left, bad);
+          else tc_convert<C, KIND, false>(base + C::kRvOff + rst * C::kRaw, sv + vst * C::kOp, ct, 0, 0, bad);
           if (bad) bad_sh = 1;
           fence_async_shared();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(smem_u32(&bar_vfull[st]));
+            mbar_arrive(smem_u32(&bar_vfull[vst]));
             mbar_arrive(smem_u32(&bar_rve[rst]));
           }
         } else {
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int r0 = max(fresh, 0);
             for (int idx = ct; idx < (kTcBN - r0) * C::kRow16; idx += 128) {
               const int row = r0 + idx / C::kRow16, c = idx % C::kRow16;
-              const uint32_t at = sv + st * C::kOp + tc_off(row, c);
+              const uint32_t at = sv + vst * C::kOp + tc_off(row, c);
               if (row >= left) {
                 sts128(at, 0u, 0u, 0u, 0u);
               } else {
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             fence_async_shared();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bar_vfull[st]));
+          if (lane == 0) mbar_arrive(smem_u32(&bar_vfull[vst]));
         }
       }
     }
@@ -563,7 +568,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           constexpr bool tail = decltype(tail_tag)::value;
           const uint64_t rs2 = f2_pack(rs, rs);
           uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
+#pragma unroll 1  // four copies of this and the other roles' code do not fit the instruction cache (295 -> 236 us)
           for (int hh = 0; hh < 4; ++hh) {
             uint32_t rr[32], pk[16];
             tmem_ld32(s_tm + 32 * hh, rr);
