@@ -11,14 +11,13 @@
 //
 // Bound: memory.  A K/V byte serves 16 or 32 rows, 32-64 flops a byte over a
 // bf16 cache, well below what mma.sync sustains; so K and V stream through a
-// ring of TMA tiles (64 tokens each) and four warps take 16 tokens of a tile
-// each.  With 16 or 32 rows a tcgen05 tile (128 rows at least) would be mostly
+// ring of TMA tiles (64 to 128 tokens) and each warp takes 16 or 32 tokens of a tile.  With 16 or 32 rows a tcgen05 tile (128 rows at least) would be mostly
 // padding, and its accumulators would have to come back through tensor memory.
 //
-// Work split: all (sequence, row tile, KV head) units, each of ceil(len / 64)
-// tiles, laid end to end, are cut into equal contiguous shares, one per CTA
-// (two CTAs per SM), whatever the lengths are; every CTA finds its share from
-// the lengths on the device, so nothing is planned on the host.  A unit inside
+// Work split: all (sequence, row tile, KV head) units of ceil(len / BN) tiles each
+// are cut into shares of equal length, one per CTA, whatever the lengths are
+// (tree_share); every CTA finds its share from the lengths on the device, so nothing
+// is planned on the host.  A unit inside
 // one share is finished there; the parts of the others go to the workspace (at
 // most two per CTA) and k_tree_join adds them up in a fixed order.
 //
@@ -89,17 +88,23 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &P, int s, int BM, 
 }
 
 struct TreeShare {
-  long long begin, end, chunk;   // tiles of this CTA; tiles per CTA
-  long long rem;                 // begin's place among the tiles of sequence s
-  int s;
+  long long begin, end, chunk;   // tiles of this CTA (laid end to end); tiles per CTA
+  long long rem;                 // its first tile's place among those of sequence s
+  int s, aligned;
 };
 
-// This CTA's share, found by all of its threads together.
+// This CTA's share, found by all of its threads together.  Tiles are laid end to
+// end and cut evenly; but starting a second unit costs a CTA about as much as a few
+// tiles, so where a share of up to kTreeSlack tiles more gives every unit CTAs of its
+// own (ceil(nt / chunk) of them, no more than there are in all), units are cut by
+// themselves.
+constexpr int kTreeSlack = 4;
 template <int NT>
 __device__ __forceinline__ void tree_share(const TreeParams &P, int BM, int BN, TreeShare *sh, long long *warp_sum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (P.nseq + NT - 1) / NT;
   const int s0 = min(tid * per, P.nseq), s1 = min(s0 + per, P.nseq);
+  __shared__ unsigned long long cand[(kTreeSlack + 2) / 2][NT / 32];
   long long own = 0;
   for (int s = s0; s < s1; ++s) {
     const TreeSeq q = tree_seq(P, s, BM, BN, blockIdx.x == 0);
@@ -119,27 +124,88 @@ __device__ __forceinline__ void tree_share(const TreeParams &P, int BM, int BN, 
     total += warp_sum[w];
   }
   inc += before;
-  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
-  const long long b = min((long long)blockIdx.x * chunk, total), e = min(b + chunk, total);
-  if (tid == 0) {
-    sh->begin = b;
-    sh->end = e;
-    sh->chunk = chunk;
-  }
-  long long at = inc - own;
-  if (b < e && b >= at && b < inc) {
+  long long chunk = (total + gridDim.x - 1) / gridDim.x;
+  long long at = inc - own, me = (long long)blockIdx.x * chunk;
+  bool aligned = false;
+  // with one tile a CTA the units are apart already; with more units than CTAs they cannot be
+  if (chunk > 1 && (long long)P.nseq * P.Hkv <= gridDim.x) {
+    // the CTAs that each longer share needs, capped so that two sums fit one word
+    constexpr int NC = kTreeSlack + 1, NW = (NC + 1) / 2;
+    unsigned long long want[NW], all[NW], upto[NW];
+#pragma unroll
+    for (int w = 0; w < NW; ++w) want[w] = 0;
     for (int s = s0; s < s1; ++s) {
       const TreeSeq q = tree_seq(P, s, BM, BN, false);
-      const long long c = (long long)q.nt * q.mt * P.Hkv;
-      if (b < at + c) {
+#pragma unroll
+      for (int k = 0; k < NC; ++k)
+        want[k / 2] += min((q.nt + chunk + k - 1) / (chunk + k) * q.mt * P.Hkv, 1ll << 20) << (32 * (k & 1));
+    }
+#pragma unroll
+    for (int w = 0; w < NW; ++w) upto[w] = want[w];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const unsigned long long v = __shfl_up_sync(0xffffffffu, upto[w], o);
+        if (lane >= o) upto[w] += v;
+      }
+    if (lane == 31) {
+#pragma unroll
+      for (int w = 0; w < NW; ++w) cand[w][warp] = upto[w];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      all[w] = 0;
+      for (int k = 0; k < NT / 32; ++k) {
+        if (k < warp) upto[w] += cand[w][k];
+        all[w] += cand[w][k];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      const int sh32 = 32 * (k & 1);
+      if (!aligned && (uint32_t)(all[k / 2] >> sh32) <= gridDim.x) {
+        aligned = true;
+        chunk += k;
+        own = (uint32_t)(want[k / 2] >> sh32);
+        at = (uint32_t)(upto[k / 2] >> sh32) - own;
+        total = (uint32_t)(all[k / 2] >> sh32);
+        me = blockIdx.x;
+      }
+    }
+  }
+  if (tid == 0) {
+    sh->chunk = chunk;
+    sh->aligned = aligned;
+    sh->begin = aligned ? 0 : min(me, total);
+    sh->end = aligned ? 0 : min(me + chunk, total);
+  }
+  __syncthreads();
+  if (me < total && me >= at && me < at + own) {
+    for (int s = s0; s < s1; ++s) {
+      const TreeSeq q = tree_seq(P, s, BM, BN, false);
+      const long long cut = q.nt > 0 ? (q.nt + chunk - 1) / chunk : 0;
+      const long long c = (aligned ? cut : q.nt) * q.mt * P.Hkv;
+      if (me < at + c) {
         sh->s = s;
-        sh->rem = b - at;
+        sh->rem = me - at;
+        if (aligned) {
+          const long long u = (me - at) / cut, part = (me - at) - u * cut;
+          sh->rem = u * q.nt + part * chunk;
+          sh->end = min(chunk, q.nt - part * chunk);
+        }
         break;
       }
       at += c;
     }
   }
   __syncthreads();
+}
+
+// The CTA with the last tile of a unit of nt tiles that begins, at tile `at` of all, in this one.
+__device__ __forceinline__ int tree_last_cta(const TreeShare &sh, long long at, int nt) {
+  return sh.aligned ? (int)(blockIdx.x + (nt - 1) / sh.chunk) : (int)((at + nt - 1) / sh.chunk);
 }
 
 // The segments of a share: consecutive tiles of one unit.
@@ -865,7 +931,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
       d.n = w.q.n;
       d.j = w.j;
       d.row_tile0 = rbase;
-      d.last = (int)((at + w.q.nt - 1) / share.chunk);
+      d.last = tree_last_cta(share, at, w.q.nt);
       P.desc[blockIdx.x] = d;
     }
     named_sync(1, NC);  // obuf and the Q fragments are free again

@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         d.n = w.q.n;
         d.j = w.j;
         d.row_tile0 = rbase;
-        d.last = (int)((at + w.q.nt - 1) / share.chunk);
+        d.last = tree_last_cta(share, at, w.q.nt);
         P.desc[blockIdx.x] = d;
       }
     }
