@@ -124,8 +124,10 @@ int fp_rope_create(int d, int rot, int layout, double theta, int scaling, double
     hi = std::fmin(std::ceil(at(low)), rot - 1.0);
   }
   bool ok = true;
-  for (int i = 0; i < rot / 2; ++i) {
-    long double f = powl(base, -2.0L * i / rot);
+  const long double step = powl(base, -2.0L / rot);
+  long double power = 1.0L;  // step^i, off by at most i 2^-63 of itself
+  for (int i = 0; i < rot / 2; ++i, power *= step) {
+    long double f = power;
     if (scaling == FP_ROPE_LINEAR) f /= factor;
     if (scaling == FP_ROPE_BANDS) {
       long double w = ((long double)orig_len * f / two_pi - low) / (high - low);
@@ -484,6 +486,7 @@ int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, 
                  int max_q, const uint64_t *mask, float scale, void *out, int64_t o_tok, int64_t o_head, float *lse,
                  void *work, size_t work_bytes, void *stream) {
   if (!kv || T < 0 || max_pages < 0 || !tree_shape_ok(nseq, max_q, Hq, kv->g.heads, kv->d)) return FP_ERR_ARG;
+  if ((int64_t)max_pages * kv->g.page > (int64_t)1 << 30) return FP_ERR_ARG;  // positions are 32-bit in the kernels
   if (dtype != FP_DT_BF16 && dtype != FP_DT_F16) return FP_ERR_ARG;
   if ((kv->dtype == FP_DT_BF16 || kv->dtype == FP_DT_F16) && kv->dtype != dtype) return FP_ERR_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return FP_ERR_ARG;

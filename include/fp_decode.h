@@ -17,8 +17,10 @@
  * boundaries (pointer and strides), unless stated.  Query head h reads KV head
  * h / (Hq/Hkv).  All pointers are of the current device; all calls are
  * asynchronous on `stream` (a cudaStream_t, NULL = legacy default stream),
- * allocate nothing on the device and may be captured into a CUDA graph.  The
- * caller keeps every buffer alive until the stream has passed the call.
+ * allocate nothing on the device and may be captured into a CUDA graph (a
+ * library call made before on the same device has done the set-up).  The
+ * caller keeps every buffer alive until the stream has passed the call; a
+ * captured call reads its tables anew at every replay.
  *
  * Errors: FP_OK or an FP_ERR_* code of fp_sparse.h; argument errors are found
  * on the host before any launch.  Tables that live on the device (slots, block
@@ -165,8 +167,8 @@ size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d);
  * included.
  *   q, out       [Hq][T][d] with strides, dtype FP_DT_BF16 or FP_DT_F16; over a
  *                bf16 or fp16 cache the cache's type
- *   block_table  device int32[nseq][max_pages], kv_len device int32[nseq],
- *                cu_q device int32[nseq+1] (cu_q[0] = 0, non-decreasing,
+ *   block_table  device int32[nseq][max_pages] (max_pages*page <= 2^30), kv_len
+ *                device int32[nseq], cu_q device int32[nseq+1] (cu_q[0] = 0, non-decreasing,
  *                cu_q[nseq] <= T), 4-byte aligned
  *   mask         device uint64[T][ceil(max_q/64)] or NULL, 8-byte aligned
  *   lse          device fp32 [Hq][T]

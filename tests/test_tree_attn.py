@@ -465,6 +465,37 @@ def test_a_decode_step_end_to_end(fp, kind):
             assert bool(((out[h, b:b + news[s]].double() - ref).abs() <= bound).all())
 
 
+@pytest.mark.parametrize("kind,dtype", [("bf16", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("n,g,count,Hkv", [(1, 2, 700, 1), (2, 16, 130, 3), (20, 4, 170, 2), (64, 4, 40, 2)])
+def test_more_sequences_than_processors(fp, kind, dtype, n, g, count, Hkv):
+    """Several units to a CTA, more sequences than a block has threads, empty ones among them."""
+    r = random.Random(19)
+    news = [r.choice([0, n, n, max(1, n // 2)]) for _ in range(count)]
+    lens = [m + r.choice([0, 3, 64, 130, 200]) for m in news]
+    Case(kind, dtype, 64, 16, Hkv, g, lens, news, masked=n > 1, seed=19, max_q=n).check(fp)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", "f16"), ("int8", "bf16")])
+@pytest.mark.parametrize("n,g", [(1, 4), (6, 4), (32, 4), (64, 4)])
+def test_lengths_that_fill_their_tiles(fp, kind, dtype, n, g):
+    Case(kind, dtype, 128, 128, 2, g, [64, 128, 256, 384, 1024], [n] * 5, masked=True, seed=20).check(fp)
+
+
+@pytest.mark.parametrize("n,g", [(3, 4), (40, 2)])
+def test_sequences_that_share_pages_and_masks_with_bits_past_the_draft(fp, n, g):
+    """Two sequences over the same prefix pages give what they give over copies of them; bits of a mask
+    from the draft's length on mean nothing."""
+    c = Case("bf16", "bf16", 128, 16, 2, g, [160 + n, 160 + n], [n, n], masked=True, seed=21, max_q=64)
+    for w in range(2):
+        for p in range(10):
+            c.pool[w][c.table[1, p].long()] = c.pool[w][c.table[0, p].long()]
+    want, wl = c.check(fp)
+    c.table[1, :10] = c.table[0, :10]
+    c.mask = c.mask | (-1 << n)
+    out, lse = c.run(fp)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
 def test_cache_past_32_bits(fp):
     """Pages whose byte offset passes 2^32."""
     c = Case("int8", "bf16", 128, 128, 8, 2, [300], [2], seed=17)
@@ -493,11 +524,14 @@ def test_refusals_of_the_binding(fp):
     for bad in (dict(q=c.q.half()), dict(q=c.q[:3], out=out[:3]), dict(q=c.q[:, :1]), dict(out=out.float()), dict(out=out[:, :1]),
                 dict(block_table=c.table.long()), dict(block_table=c.table[0]), dict(kv_len=c.len.long()), dict(cu_q=c.cu[:1]),
                 dict(mask=c.mask.int()), dict(mask=c.mask[:1]), dict(max_q=0), dict(max_q=257), dict(max_q=100),
-                dict(scale=float("nan")), dict(work=work[:-256]), dict(work=work[8:]), dict(work=work.cpu()),
+                dict(scale=float("nan")), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("inf")), dict(work=work[:-256]), dict(work=work[8:]), dict(work=work.cpu()),
                 dict(lse=torch.empty(4, 1, device="cuda")), dict(kv_len=c.len.cpu())):
         with pytest.raises(fp.FpError) as e:
             fp.fp_tree_attn(**{**ok, **bad})
         assert e.value.code == fp.FP_ERR_ARG, bad
+    wide = torch.zeros(1, (1 << 26) + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(fp.FpError):
+        fp.fp_tree_attn(**{**ok, "block_table": wide})   # positions past 2^30
     h = fp.KvCache(c.pool[0].half(), c.pool[1].half())
     with pytest.raises(fp.FpError):
         fp.fp_tree_attn(**{**ok, "kv": h})          # bf16 queries over an fp16 cache
