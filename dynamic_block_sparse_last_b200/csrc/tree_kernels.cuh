@@ -377,6 +377,7 @@ struct TreeCfg {
   // Registers when kBig: the block starts with 168 a thread (384 threads), and 2 x 128 x 216 + 128 x 56 = 62464 <= 384 x 168.
   static constexpr int kRegs = 216, kRegsTma = 56;
   static constexpr int TOK = (kQuant && MT == 1) || D == 64 ? 32 : 16;  // tokens of a warp in a tile
+  static constexpr bool kQReg = MT == 1 && !(kQuant && D == 128);  // Q in registers
   static constexpr int BN = kWarps * TOK;                 // tokens of a tile
   static constexpr int RB = D * KvCode<KIND>::kBytes;     // bytes of a cached row
   static constexpr int kBoxB = RB < 128 ? RB : 128;       // bytes of a box row
@@ -559,8 +560,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
       if (lane == 0) row_scale[r] = fac * P.scale2;
     }
     named_sync(1, NC);
-    uint32_t qf[MT == 1 ? C::kSteps : 1][4];
-    if constexpr (MT == 1) {
+    uint32_t qf[C::kQReg ? C::kSteps : 1][4];
+    if constexpr (C::kQReg) {
 #pragma unroll
       for (int k = 0; k < C::kSteps; ++k) {
         const uint4 x = lds128(qbase + (k * 32 + lane) * 16);
