@@ -23,7 +23,7 @@
 //
 // Measured (32 query heads, 8 KV heads of 128): 64 sequences of up to 16384 tokens,
 // one new token each, over bf16 in 365 us, 6.4 TB/s (0.97 of the measured copy); over
-// int8 in 239 us, 5.0 TB/s: there a warp's chain of conversion, product, softmax and
+// int8 in 231 us, 5.2 TB/s (244 us after seconds under load, as the clock falls): there a warp's chain of conversion, product, softmax and
 // product is what two warps a scheduler do not hide (issue slots 43% busy).
 //
 // Operand order: a matrix product does not mind the order of its inner index,
@@ -377,7 +377,9 @@ struct TreeCfg {
   // Registers when kBig: the block starts with 168 a thread (384 threads), and 2 x 128 x 216 + 128 x 56 = 62464 <= 384 x 168.
   static constexpr int kRegs = 216, kRegsTma = 56;
   static constexpr int TOK = (kQuant && MT == 1) || D == 64 ? 32 : 16;  // tokens of a warp in a tile
-  static constexpr bool kQReg = MT == 1 && !(kQuant && D == 128);  // Q in registers
+  // Q in registers, except where they are short: read again for every 32 tokens then
+  // (int8 decode batch, 64 sequences of up to 16384 tokens: 231 us against 243)
+  static constexpr bool kQReg = MT == 1 && !(kQuant && D == 128);
   static constexpr int BN = kWarps * TOK;                 // tokens of a tile
   static constexpr int RB = D * KvCode<KIND>::kBytes;     // bytes of a cached row
   static constexpr int kBoxB = RB < 128 ? RB : 128;       // bytes of a box row
@@ -632,7 +634,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
               uint32_t a[4];
-              if constexpr (MT == 1) {
+              if constexpr (C::kQReg) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a[e] = qf[step][e];
               } else {
