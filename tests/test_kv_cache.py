@@ -173,6 +173,28 @@ def test_extreme_and_non_finite_rows(fp):
     assert bool(((out[0, fine].double() - k[0, fine].double()).abs() <= M / 254 * (1 + 2.0 ** -20) + 127 * 2.0 ** -149).all())
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_non_finite_and_extreme_16_bit_rows(fp, kind, dtype):
+    d, dt = 64, TYPES[dtype]
+    top, low = (3e38, 1e-38) if dtype == "bf16" else (6e4, 2e-6)
+    p = pools(kind, 1, 2, 16, d)
+    kv = fp.KvCache(*p)
+    k = rand((2, 9, d), torch.float32, 10)
+    k[:, 0] *= top / k[:, 0].abs().amax(-1, keepdim=True)
+    k[:, 1] *= low / k[:, 1].abs().amax(-1, keepdim=True)
+    k = k.to(dt)
+    k[0, 2, 63], k[1, 3, 0], k[0, 4, 17], k[1, 4, 18] = float("nan"), float("inf"), -float("inf"), float("nan")
+    kv.write(k, k, torch.arange(9, device="cuda"))
+    out = torch.empty(2, 9, d, device="cuda")
+    kv.read(torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([0, 9], dtype=torch.int32, device="cuda"), out, None)
+    bad = ~torch.isfinite(k).all(-1)
+    assert bool(torch.isnan(out[bad]).all()) and bool(torch.isfinite(out[~bad]).all())
+    code, _ = codes_of(k.transpose(0, 1), kind, True)
+    got = raw(p[0])[0].view(CODES[kind][0])[:, :9].float()
+    assert torch.equal(got[~bad], code.transpose(0, 1)[~bad]) and float(got[bad].abs().max()) == 0
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3", "bf16", "f16"])
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("d,page", [(128, 16), (64, 64), (128, 128)])
