@@ -11,8 +11,9 @@
 //
 // Bound: memory.  A K/V byte serves 16 or 32 rows, 32-64 flops a byte over a
 // bf16 cache, well below what mma.sync sustains; so K and V stream through a
-// ring of TMA tiles (64 to 128 tokens) and each warp takes 16 or 32 tokens of a tile.  With 16 or 32 rows a tcgen05 tile (128 rows at least) would be mostly
-// padding, and its accumulators would have to come back through tensor memory.
+// ring of TMA tiles (64 to 128 tokens) and each warp takes 16 or 32 tokens of a tile.
+// With 16 or 32 rows a tcgen05 tile (128 rows at least) would be mostly padding, and
+// its accumulators would have to come back through tensor memory.
 //
 // Work split: all (sequence, row tile, KV head) units of ceil(len / BN) tiles each
 // are cut into shares of equal length, one per CTA, whatever the lengths are
@@ -23,8 +24,9 @@
 //
 // Measured (32 query heads, 8 KV heads of 128): 64 sequences of up to 16384 tokens,
 // one new token each, over bf16 in 365 us, 6.4 TB/s (0.97 of the measured copy); over
-// int8 in 231 us, 5.2 TB/s (244 us after seconds under load, as the clock falls): there a warp's chain of conversion, product, softmax and
-// product is what two warps a scheduler do not hide (issue slots 43% busy).
+// int8 in 231 us, 5.2 TB/s (244 us after seconds under load, as the clock falls):
+// there a warp's chain of conversion, product, softmax and product is what two warps
+// a scheduler do not hide (issue slots 49% busy).
 //
 // Operand order: a matrix product does not mind the order of its inner index,
 // so K is taken in the order in which a thread's 16-byte shared-memory reads
@@ -35,6 +37,13 @@
 // so far (kexp) so that they keep fp16's range.  bf16 queries over a quantised
 // cache are brought to fp16 by a power of two per row, exactly (elements below
 // 2^-14 of the row's largest lose bits from 2^-25 of it on).
+//
+// Rounding: the products take P (times V's scale) in 16 bits, bf16 over bf16 caches and
+// fp16 elsewhere, off by at most 2^-8 or 2^-11 of each probability: as much again as
+// out's own rounding has.  With many tokens these errors average out; where one token
+// dominates a row they are common to its columns.  The sums are of the unrounded
+// values: sums of the rounded ones would make a dominated row exact, but they would bring
+// P's rounding into lse and double the bound of the others.
 #pragma once
 
 #include <type_traits>
