@@ -352,7 +352,9 @@ __device__ __forceinline__ uint32_t tree_clean(uint32_t w, int &bad) {
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
 
+// A barrier of some warps of the block; each takes part as a whole, so its lanes meet first.
 __device__ __forceinline__ void named_sync(int id, int threads) {
+  __syncwarp();
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
@@ -810,6 +812,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
                   else if (pos >= prefix) vw[e][k] = tree_clean<KIND>(vw[e][k], bad);
                 }
               }
+              __syncwarp();  // the products take the warp together
             }
             if constexpr (C::kQuant) {
 #pragma unroll

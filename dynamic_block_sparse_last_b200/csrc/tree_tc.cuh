@@ -738,26 +738,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(__uint_as_float(o1[e]), f1, __uint_as_float(o[e])));
           }
-          if (!have) continue;
-          if (whole) {
-            uint16_t *dst = static_cast<uint16_t *>(P.out) + (w.q.row0 + tk) * P.o_tok + h * P.o_head + col;
+          if (have) {
+            if (whole) {
+              uint16_t *dst = static_cast<uint16_t *>(P.out) + (w.q.row0 + tk) * P.o_tok + h * P.o_head + col;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t y[4];
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t y[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float a = __uint_as_float(o[e + 2 * q]), b = __uint_as_float(o[e + 2 * q + 1]);
-                y[q] = P.q_f16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+                for (int q = 0; q < 4; ++q) {
+                  const float a = __uint_as_float(o[e + 2 * q]), b = __uint_as_float(o[e + 2 * q + 1]);
+                  y[q] = P.q_f16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+                }
+                *reinterpret_cast<uint4 *>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
               }
-              *reinterpret_cast<uint4 *>(dst + e) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-          } else {
-            float *dst = P.part + ((int64_t)slot * C::BM + trow) * D + col;
+            } else {
+              float *dst = P.part + ((int64_t)slot * C::BM + trow) * D + col;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4 *>(dst + e) = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
-                                                                 __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4 *>(dst + e) = make_float4(__uint_as_float(o[e]), __uint_as_float(o[e + 1]),
+                                                                   __uint_as_float(o[e + 2]), __uint_as_float(o[e + 3]));
+            }
           }
+          __syncwarp();  // the next load from tensor memory takes the warp together
         }
       }
       if (have && *(volatile int *)&bad_sh) {
@@ -786,6 +788,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
   }
+  __syncwarp();  // the roles' branches leave lanes apart; what follows takes whole warps
   tc_fence_before();
   __syncthreads();
   if (warp == kMma) {

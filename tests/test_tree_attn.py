@@ -537,3 +537,10 @@ def test_refusals_of_the_binding(fp):
         fp.fp_tree_attn(**{**ok, "kv": h})          # bf16 queries over an fp16 cache
     torch.cuda.synchronize()
     assert fp.fp_get_device_error() == fp.FP_OK
+
+
+@pytest.mark.parametrize("kind,dtype", [("bf16", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("n", [33, 47, 63, 65, 97, 127, 129, 161, 200, 255])
+def test_rows_that_end_inside_a_warp(fp, kind, dtype, n):
+    """Units whose last warp has rows for some of its lanes only, finished by one processor and split over several."""
+    Case(kind, dtype, 128, 64, 1, 1, [n + 40, n + 3000], [n, n], masked=True, seed=22).check(fp)
