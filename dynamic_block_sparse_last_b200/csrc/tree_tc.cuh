@@ -25,7 +25,9 @@
 // largest, then the exponentials, P written over columns of S that are read already
 // (whole rows in registers spilled, and with 192 KB of operands there is no L1 to
 // spill to).  The row's reference moves only when P would leave its type's range, and
-// then by a whole power of two, so that the P already written is scaled exactly.
+// then by a whole power of two: the P of the tile that is already written is scaled in
+// fp32 and rounded again, which changes only what becomes smaller than the type's
+// smallest normal number.
 // Sums are of the unrounded exponentials.
 //
 // Measured (32 query heads, 8 KV heads of 128): 64 drafted tokens over 131072 cached in
@@ -117,14 +119,16 @@ __device__ __forceinline__ void tc_ld_wait16(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
-// Two packed 16-bit values times a power of two.
+// Two packed 16-bit values times a power of two, which may be below fp16's range (the values
+// are up to 2^15, so the products need not be).
 template <int KIND>
 __device__ __forceinline__ uint32_t tc_scale2(uint32_t x, float by) {
-  const uint32_t b = KIND == kKvBf16 ? pack_bf16x2(by, by) : pack_f16x2(by, by);
-  uint32_t r;
-  if constexpr (KIND == kKvBf16) asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(b));
-  else asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(b));
-  return r;
+  if constexpr (KIND == kKvBf16) {
+    return pack_bf16x2(__uint_as_float(x << 16) * by, __uint_as_float(x & 0xffff0000u) * by);
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&x));
+    return pack_f16x2(f.x * by, f.y * by);
+  }
 }
 
 // Instruction descriptor as idesc_bf16, operand format 0 = fp16 or 1 = bf16.
@@ -607,8 +611,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int e = 4; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(rr[e]));
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * rs;  // rs > 0
             if (__any_sync(0xffffffffu, mx > m_ref + C::kSlack)) {
-              // the reference moves, by whole powers of two, so that what was made
-              // against the old one (sums, the P of the chunks before) scales exactly
+              // the reference moves, by whole powers of two: the sums scale exactly, and so
+              // do the P of the chunks before as far as their type goes
               const bool mine = mx > m_ref + C::kSlack;
               const float to = mine ? ceilf(mx) : m_ref;
               const float by = !mine ? 1.f : (to - m_ref < 126.f ? pow2i((int)(m_ref - to)) : 0.f);
