@@ -33,10 +33,19 @@
 // bring it (Q's registers follow), and V's columns likewise: no ldmatrix, no
 // transposition through shared memory.  Quantised K and V are multiplied as
 // their codes, which fp16 holds exactly; K's scale goes to the scores and V's
-// to the probabilities, taken relative to a power of two near the largest seen
-// so far (kexp) so that they keep fp16's range.  bf16 queries over a quantised
+// to the probabilities.  bf16 queries over a quantised
 // cache are brought to fp16 by a power of two per row, exactly (elements below
 // 2^-14 of the row's largest lose bits from 2^-25 of it on).
+//
+// Units: a row's weights w_p = 2^(s_p - m) times V's scale (1 where there is none) and its sum of
+// 2^(s_p - m) are taken in one unit 2^m, m a whole number.  It moves only when a weight
+// of the row passes 2^(kLift + kSlack), and then so that the row's largest is at most
+// 2^kLift; sum and O are rescaled exactly.  It is the row's own: what a row does not
+// see, or sees without weight, whatever V row it has, moves nothing of it: a bound that
+// takes a row's largest score with the largest of some tokens' scales only says when to
+// look at the products themselves.  Parts are
+// added up relative to the row's sum, not to their units, which V's scales may set
+// far apart (tree_top).
 //
 // Rounding: the products take P (times V's scale) in 16 bits, bf16 over bf16 caches and
 // fp16 elsewhere, off by at most 2^-8 or 2^-11 of each probability: as much again as
@@ -351,6 +360,27 @@ __device__ __forceinline__ uint32_t tree_clean(uint32_t w, int &bad) {
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) << 23); }  // -126 <= e <= 127
+// 2^d of a whole number d <= 127, 0 below fp32's normal range.
+__device__ __forceinline__ float tree_pow2(float d) { return d < -126.f ? 0.f : pow2i((int)d); }
+
+// What a row's weights are taken in (see Units above).
+template <int KIND>
+struct TreeUnit {
+  static constexpr float kLift = 0.f;
+  static constexpr float kSlack = KIND == kKvBf16 ? 40.f : 14.f;  // fp16 holds up to 2^15.99
+  static constexpr float kFar = 70.f;  // 2^(s - m) stays below about 2^kFar over V rows of next to nothing
+  // the unit of a row whose largest product is 2^key and whose largest score is top
+  static __device__ __forceinline__ float at(float key, float top) { return ceilf(fmaxf(key, top - kFar)) - kLift; }
+  // log2 of the largest of some V scales, as the bound takes it
+  static __device__ __forceinline__ float bound(float lv) { return fmaxf(lv, -kFar) - (kLift + kSlack); }
+};
+
+// The power of two (log2) below the sum l of a row in units of 2^m; -inf for 0.
+__device__ __forceinline__ float tree_top(float m, float l) {
+  return l == 0.f ? -INFINITY : m + (float)((int)((__float_as_uint(l) >> 23) & 0xffu) - 127);
+}
+// log2 of a V scale; -inf for one that sets no unit (0, or not finite).
+__device__ __forceinline__ float tree_log2(float v) { return v > 0.f && v < INFINITY ? __log2f(v) : -INFINITY; }
 
 // A barrier of some warps of the block; each takes part as a whole, so its lanes meet first.
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -408,9 +438,6 @@ struct TreeCfg {
   static constexpr int kLd = D + 4;                       // row pitch of obuf (fp32)
   static constexpr int kOOff = kQOff + MT * kSteps * 512;
   static constexpr int kSmem = kOOff + BM * kLd * 4 + 1024;
-  // A row's reference moves when one of its scores passes it by more than this (log2
-  // units), as far as P's type goes: fp16 2^14, times V scales below 2; bf16 2^40.
-  static constexpr float kSlack = KIND == kKvBf16 ? 40.f : 14.f;
 };
 
 // Shared address of the 16-byte chunk `ch` of row r of a tile (TMA swizzle:
@@ -598,8 +625,6 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
       m[mt][0] = m[mt][1] = -INFINITY;
       l[mt][0] = l[mt][1] = 0.f;
     }
-    int kexp = -126;                   // V's scales are taken relative to 2^kexp: kinv = 2^-kexp,
-    float klim = 0.f, kinv = pow2i(126);  // and below klim = 2^(kexp + 1) (0 at first, so that the first one sets it)
     int bad = 0;
     for (int t = w.a; t < w.b; ++t, ++u) {
       const int st = u % C::kStages;
@@ -703,9 +728,16 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
               if (pos0 + 8 * (k >> 1) + 2 * c4 + (k & 1) >= w.q.len) vs[k] = 0.f;
           }
         }
-        // ---- softmax against the rows' references.  In the common case no thread's
-        // values ask for more than a vote; only then do the four lanes of a row agree
-        // on its largest score, and the warp on the largest V scale.
+        // ---- weights in the rows' units.  In the common case no thread's values ask for
+        // more than a vote; only then do the four lanes of a row agree on its unit.
+        using U = TreeUnit<KIND>;
+        float lim = -(U::kLift + U::kSlack);
+        if constexpr (C::kQuant) {
+          float vmx = vs[0];
+#pragma unroll
+          for (int k = 1; k < 2 * NT; ++k) vmx = fmaxf(vmx, vs[k]);
+          lim = U::bound(__log2f(vmx));
+        }
         float mxl[MT][2];
         bool ask = false;
 #pragma unroll
@@ -716,50 +748,42 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
 #pragma unroll
             for (int i = 1; i < NT; ++i) mx = fmaxf(mx, fmaxf(s[mt][i][2 * hh], s[mt][i][2 * hh + 1]));
             mxl[mt][hh] = mx;
-            ask |= mx > m[mt][hh] + C::kSlack;
+            ask |= mx + lim > m[mt][hh];
           }
-        [[maybe_unused]] float vmx = 0.f;
-        if constexpr (C::kQuant) {
-#pragma unroll
-          for (int k = 0; k < 2 * NT; ++k) vmx = fmaxf(vmx, vs[k]);
-          ask |= vmx >= klim && vmx < INFINITY;  // a NaN scale does not count
-        }
         if (__any_sync(0xffffffffu, ask)) {
-          float kfac = 1.f;
+          [[maybe_unused]] float lv[2 * NT];
           if constexpr (C::kQuant) {
-            vmx = vmx < INFINITY ? vmx : 0.f;
-            vmx = redux_max_f32(vmx);
-            if (vmx >= klim) {  // V's scales relative to 2^kexp stay below 2
-              const int e = min((int)(__float_as_uint(vmx) >> 23) - 127, 125);
-              kfac = e - kexp > 126 ? 0.f : pow2i(kexp - e);
-              kexp = e;
-              klim = pow2i(e + 1);
-              kinv = pow2i(-e);
-            }
+#pragma unroll
+            for (int k = 0; k < 2 * NT; ++k) lv[k] = tree_log2(vs[k]);
           }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
             float al[2];
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
-              float mx = mxl[mt][hh];
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              const float mn = mx > m[mt][hh] + C::kSlack ? mx : m[mt][hh];
-              al[hh] = mn > m[mt][hh] ? ex2(m[mt][hh] - mn) : 1.f;
-              m[mt][hh] = mn;
+              float top = mxl[mt][hh], key = C::kQuant ? -INFINITY : top;
+              if constexpr (C::kQuant) {
+#pragma unroll
+                for (int k = 0; k < 2 * NT; ++k) key = fmaxf(key, s[mt][k >> 1][2 * hh + (k & 1)] + lv[k]);
+              }
+#pragma unroll
+              for (int x = 1; x < 4; x <<= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                key = fmaxf(key, __shfl_xor_sync(0xffffffffu, key, x));
+              }
+              const float to = U::at(key, top);
+              al[hh] = 1.f;
+              if (to > m[mt][hh] + U::kSlack) {
+                al[hh] = tree_pow2(m[mt][hh] - to);
+                m[mt][hh] = to;
+              }
               l[mt][hh] *= al[hh];
-              al[hh] *= kfac;
             }
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
 #pragma unroll
               for (int e = 0; e < 4; ++e) o[mt][i][e] *= al[e >> 1];
           }
-        }
-        if constexpr (C::kQuant) {
-#pragma unroll
-          for (int k = 0; k < 2 * NT; ++k) vs[k] *= kinv;
         }
         uint32_t pa[MT][NB][4];
 #pragma unroll
@@ -866,14 +890,14 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         const int r = 16 * mt + 8 * hh + q4;
-        float M = red_m[0][r];
+        float M = tree_top(red_m[0][r], red_l[0][r]);
 #pragma unroll
-        for (int k = 1; k < C::kWarps; ++k) M = fmaxf(M, red_m[k][r]);
+        for (int k = 1; k < C::kWarps; ++k) M = fmaxf(M, tree_top(red_m[k][r], red_l[k][r]));
         const float ref = M == -INFINITY ? 0.f : M;
         float L = 0.f;
 #pragma unroll
-        for (int k = 0; k < C::kWarps; ++k) L += red_l[k][r] * ex2(red_m[k][r] - ref);
-        f[mt][hh] = ex2(m[mt][hh] - ref) * (C::kQuant ? pow2i(kexp) : 1.f);
+        for (int k = 0; k < C::kWarps; ++k) L += red_l[k][r] * tree_pow2(red_m[k][r] - ref);
+        f[mt][hh] = tree_pow2(m[mt][hh] - ref);
         if (warp == 0 && c4 == 0) {
           fin_m[r] = M;
           fin_l[r] = L;
@@ -936,7 +960,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
         if (P.q_f16) y = make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w));
         else y = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + (w.q.row0 + i) * P.o_tok + h * P.o_head + col) = y;
-        if (col == 0 && P.lse) P.lse[(int64_t)h * P.T + w.q.row0 + i] = L == 0.f ? -INFINITY : (fin_m[r] + __log2f(L)) * kLn2;
+        if (col == 0 && P.lse) P.lse[(int64_t)h * P.T + w.q.row0 + i] = L == 0.f ? -INFINITY : (fin_m[r] + log2f(L)) * kLn2;
       } else {
         *reinterpret_cast<float4 *>(P.part + ((int64_t)slot * C::BM + r) * D + col) = v;
         if (col == 0) {
@@ -962,7 +986,8 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
 // Adds up the parts of the units that several CTAs share, in the order of the
 // CTAs.  grid (C, row groups), a warp per row (D = 64: two rows), a lane per 4
 // columns.  A latency, not a bandwidth: so the first 16 parts are under way before
-// their weights 2^(m - M) are known, which the lanes work out a part each.
+// their weights 2^(m - M) are known, which the lanes work out a part each (M: the
+// largest tree_top of the row's parts).
 template <int D>
 __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeParams P, int BM) {
   constexpr int G = D / 4, RPB = 256 / G, NP = 16;
@@ -986,8 +1011,11 @@ __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeP
   };
   load(0);
   const float2 first = ml_of(gl);
-  float M = first.x;
-  for (int k = gl + G; k < parts; k += G) M = fmaxf(M, ml_of(k).x);
+  float M = tree_top(first.x, first.y);
+  for (int k = gl + G; k < parts; k += G) {
+    const float2 ml = ml_of(k);
+    M = fmaxf(M, tree_top(ml.x, ml.y));
+  }
 #pragma unroll
   for (int o = G / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(gm, M, o));
   const float ref = M == -INFINITY ? 0.f : M;
@@ -995,7 +1023,7 @@ __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeP
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < parts; k0 += G) {
     const float2 ml = k0 == 0 ? first : ml_of(k0 + gl);
-    const float f = ex2(ml.x - ref);
+    const float f = tree_pow2(ml.x - ref);
     float lsum = ml.y * f;
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) lsum += __shfl_xor_sync(gm, lsum, o);
@@ -1018,7 +1046,7 @@ __global__ void __launch_bounds__(256) k_tree_join(const __grid_constant__ TreeP
   if (P.q_f16) y = make_uint2(pack_f16x2(acc.x * inv, acc.y * inv), pack_f16x2(acc.z * inv, acc.w * inv));
   else y = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(P.out) + (d.seq_row0 + i) * P.o_tok + h * P.o_head + col) = y;
-  if (col == 0 && P.lse) P.lse[(int64_t)h * P.T + d.seq_row0 + i] = L == 0.f ? -INFINITY : (M + __log2f(L)) * kLn2;
+  if (col == 0 && P.lse) P.lse[(int64_t)h * P.T + d.seq_row0 + i] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 }  // namespace fpk

@@ -24,10 +24,9 @@
 // Softmax: 32 scores of a row at a time, each read once from tensor memory: their
 // largest, then the exponentials, P written over columns of S that are read already
 // (whole rows in registers spilled, and with 192 KB of operands there is no L1 to
-// spill to).  The row's reference moves only when P would leave its type's range, and
-// then by a whole power of two: the P of the tile that is already written is scaled in
-// fp32 and rounded again, which changes only what becomes smaller than the type's
-// smallest normal number.
+// spill to).  Where a row's unit moves (Units in tree_kernels.cuh), the P of the tile
+// that is already written is scaled in fp32 and rounded again, which changes only what
+// becomes smaller than the type's smallest normal number.
 // Sums are of the unrounded exponentials.
 //
 // Measured (32 query heads, 8 KV heads of 128): 64 drafted tokens over 131072 cached in
@@ -70,10 +69,6 @@ struct TcCfg {
   static constexpr int kRsOff = kEnd;                     // raw scales [stage][K, V][128] fp32
   static constexpr int kSmem = kRsOff + (kQuant ? kStages * 1024 : 0) + 1024;
   static constexpr int kSc = 4;                           // scale ring
-  // A row's reference moves when a score passes it by more than this (log2
-  // units): as far as P's type goes (fp16: 2^14, times V scales below 2; bf16:
-  // 2^40, fp32's sums of P V keep their distance to 2^127), so O is seldom rescaled.
-  static constexpr float kSlack = KIND == kKvBf16 ? 40.f : 14.f;
 };
 
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -253,10 +248,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(8) uint64_t bar_q[2], bar_rkf[C::kStages], bar_rke[C::kStages], bar_rvf[C::kStages],
       bar_rve[C::kStages], bar_kfull[C::kOpsK], bar_kempty[C::kOpsK], bar_vfull[C::kOpsV], bar_vempty[C::kOpsV], bar_sfull[2],
       bar_pfull[2], bar_odone[2], bar_scfull[C::kSc], bar_scempty[C::kSc];
-  __shared__ __align__(16) float sc_k[C::kSc][kTcBN], sc_v[C::kSc][kTcBN];
-  __shared__ int sc_exp[C::kSc];
+  __shared__ __align__(16) float sc_k[C::kSc][kTcBN], sc_v[C::kSc][kTcBN], sc_l[C::kSc][kTcBN];  // sc_l: log2 of sc_v,
+  __shared__ float sc_m[C::kSc][4];                                                                      // and bounds of 32
   __shared__ float row_scale[PAIR ? 2 : 1][128], x_m[2][128], x_l[2][128];
-  __shared__ int x_exp[2];
   __shared__ long long warp_sum[kTcThreads / 32];
   __shared__ TreeShare share;
   __shared__ uint32_t tmem_sh;
@@ -422,10 +416,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp >= 8 && warp < kMma) {
     // ------------------------------------------------------------ K and V
     const int cw = warp - 8, ct = threadIdx.x - 256;
-    int u = 0, kexp = -126, bad = 0;
+    int u = 0, bad = 0;
     bool ok = true;
     for (; more && ok; more = w.next(P, C::BM, kTcBN)) {
-      kexp = -126;
       for (int t = w.a; t < w.b; ++t, ++u) {
         const int rst = u % C::kStages, kst = u % C::kOpsK, vst = u % C::kOpsV;
         const uint32_t rph = (u / C::kStages) & 1, kph = ((u / C::kOpsK) - 1) & 1, vph = ((u / C::kOpsV) - 1) & 1;
@@ -433,7 +426,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if constexpr (C::kQuant) {
           ok = mbar_wait(smem_u32(&bar_rkf[rst]), rph, abort_flag, P.err);
           if (cw == 0) {
-            // the scales of four tokens a lane: V's relative to 2^kexp, below 2
+            // the scales of four tokens a lane
             const int ss = u % C::kSc;
             if (ok && u >= C::kSc) ok = mbar_wait(smem_u32(&bar_scempty[ss]), ((u / C::kSc) - 1) & 1, abort_flag, P.err);
             const uint4 a = lds128(base + C::kRsOff + rst * 1024 + lane * 16), b = lds128(base + C::kRsOff + rst * 1024 + 512 + lane * 16);
@@ -451,13 +444,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 bad = 1;
               }
             }
-            const float mx = redux_max_f32(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])));
-            const int e = mx < INFINITY ? min((int)(__float_as_uint(mx) >> 23) - 127, 126) : -127;
-            kexp = max(kexp, e);
-            const float kinv = pow2i(-kexp);
             *reinterpret_cast<float4 *>(&sc_k[ss][4 * lane]) = make_float4(ks[0], ks[1], ks[2], ks[3]);
-            *reinterpret_cast<float4 *>(&sc_v[ss][4 * lane]) = make_float4(vs[0] * kinv, vs[1] * kinv, vs[2] * kinv, vs[3] * kinv);
-            if (lane == 0) sc_exp[ss] = kexp;
+            *reinterpret_cast<float4 *>(&sc_v[ss][4 * lane]) = make_float4(vs[0], vs[1], vs[2], vs[3]);
+            const float4 lv = make_float4(tree_log2(vs[0]), tree_log2(vs[1]), tree_log2(vs[2]), tree_log2(vs[3]));
+            *reinterpret_cast<float4 *>(&sc_l[ss][4 * lane]) = lv;
+            float lm = fmaxf(fmaxf(lv.x, lv.y), fmaxf(lv.z, lv.w));
+#pragma unroll
+            for (int x = 1; x < 8; x <<= 1) lm = fmaxf(lm, __shfl_xor_sync(0xffffffffu, lm, x));
+            if ((lane & 7) == 0) sc_m[ss][lane >> 3] = TreeUnit<KIND>::bound(lm);
             if (bad) bad_sh = 1;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bar_scfull[ss]));
@@ -559,8 +553,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool live = (PAIR ? t * 128 : 0) + (warp & 3) * 32 < R;  // the warp has rows at all
       const int tk = min(grow / P.g, w.q.n - 1);
       const float rs = row_scale[PAIR ? t : 0][row];
-      float m_ref = -INFINITY, l = 0.f;
-      int kexp = -126;
+      float m_ref = -INFINITY, l = 0.f;  // the row's unit (log2) and its sum in it
       const int L = w.b - w.a, cnt = PAIR ? L : (L - t + 1) / 2;  // tiles of this group
       for (int j = 0; j < cnt && ok; ++j, ++n) {
         const int tile = PAIR ? j : 2 * j + t, u = u0 + tile, ss = u % C::kSc;
@@ -577,6 +570,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         auto rows_of_tile = [&](auto tail_tag) __attribute__((always_inline)) {
           constexpr bool tail = decltype(tail_tag)::value;
           const uint64_t rs2 = f2_pack(rs, rs);
+          using U = TreeUnit<KIND>;
           uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll 1  // four copies of this and the other roles' code do not fit the instruction cache (295 -> 236 us)
           for (int hh = 0; hh < 4; ++hh) {
@@ -609,20 +603,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int e = 0; e < 4; ++e) mx4[e] = __uint_as_float(rr[e]);
 #pragma unroll
             for (int e = 4; e < 32; ++e) mx4[e & 3] = fmaxf(mx4[e & 3], __uint_as_float(rr[e]));
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * rs;  // rs > 0
-            if (__any_sync(0xffffffffu, mx > m_ref + C::kSlack)) {
-              // the reference moves, by whole powers of two: the sums scale exactly, and so
-              // do the P of the chunks before as far as their type goes
-              const bool mine = mx > m_ref + C::kSlack;
-              const float to = mine ? ceilf(mx) : m_ref;
-              const float by = !mine ? 1.f : (to - m_ref < 126.f ? pow2i((int)(m_ref - to)) : 0.f);
-              m_ref = to;
+            const float top = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * rs;  // rs > 0
+            float lim = -(U::kLift + U::kSlack);
+            if constexpr (C::kQuant) lim = sc_m[ss][hh];
+            if (__any_sync(0xffffffffu, top + lim > m_ref)) {
+              // the unit moves, by whole powers of two: the sums scale exactly, and so do the
+              // P of the chunks before as far as their type goes
+              float key = C::kQuant ? -INFINITY : top;
+              if constexpr (C::kQuant) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 l4 = *reinterpret_cast<const float4 *>(&sc_l[ss][hh * 32 + e]);
+                  key = fmaxf(key, fmaf(__uint_as_float(rr[e]), rs, l4.x));
+                  key = fmaxf(key, fmaf(__uint_as_float(rr[e + 1]), rs, l4.y));
+                  key = fmaxf(key, fmaf(__uint_as_float(rr[e + 2]), rs, l4.z));
+                  key = fmaxf(key, fmaf(__uint_as_float(rr[e + 3]), rs, l4.w));
+                }
+              }
+              const float to = U::at(key, top);
+              const bool mine = to > m_ref + U::kSlack;
+              const float by = mine ? tree_pow2(m_ref - to) : 1.f;
+              m_ref = mine ? to : m_ref;
               moved |= mine;
               alpha *= by;
               const uint64_t by2 = f2_pack(by, by);
 #pragma unroll
               for (int e = 0; e < 4; ++e) acc[e] = f2_mul(acc[e], by2);
-              if (hh > 0) {
+              if (hh > 0 && __any_sync(0xffffffffu, mine)) {
                 tmem_st_wait();
 #pragma unroll 1
                 for (int k = 0; k < hh; ++k) {
@@ -662,14 +669,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (pos0 + kTcBN > prefix) rows_of_tile(std::true_type{});
         else rows_of_tile(std::false_type{});
         l = l * alpha + sum;
-        if constexpr (C::kQuant) {
-          const int ke = sc_exp[ss];
-          if (ke != kexp) {  // V's scales are taken relative to another power of two from here on
-            alpha *= ke - kexp > 126 ? 0.f : pow2i(kexp - ke);
-            kexp = ke;
-            moved = true;
-          }
-        }
         // S was signalled after the group's product before had completed: O is stable here
         if (j > 0 && __any_sync(0xffffffffu, moved)) {
 #pragma unroll 1
@@ -697,7 +696,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if constexpr (!PAIR) {
         x_m[t][row] = m_ref;
         x_l[t][row] = l;
-        if (row == 0) x_exp[t] = kexp;
         named_sync(2, 256);
       }
       if (!ok) continue;
@@ -705,18 +703,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // O_0 f0 + O_1 f1 over columns [c0, c1): PAIR: this group's rows; else both groups' parts of the same rows
       float f0, f1 = 0.f, M = m_ref, Ls = l;
       if constexpr (PAIR) {
-        f0 = C::kQuant ? pow2i(kexp) : 1.f;
+        f0 = 1.f;
       } else {
         const float m0 = x_m[0][row], m1 = x_m[1][row];
-        M = fmaxf(m0, m1);
+        M = fmaxf(tree_top(m0, x_l[0][row]), tree_top(m1, x_l[1][row]));
         const float ref = M == -INFINITY ? 0.f : M;
-        f0 = ex2(m0 - ref);
-        f1 = ex2(m1 - ref);
+        f0 = tree_pow2(m0 - ref);
+        f1 = tree_pow2(m1 - ref);
         Ls = x_l[0][row] * f0 + x_l[1][row] * f1;
-        if (C::kQuant) {
-          f0 *= pow2i(x_exp[0]);
-          f1 *= pow2i(x_exp[1]);
-        }
       }
       const bool whole = w.a == 0 && w.b == w.q.nt;
       const int slot = 2 * blockIdx.x + (w.a == 0 ? 1 : 0);
@@ -774,7 +768,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (have && (PAIR || t == 0)) {
         if (whole) {
-          if (P.lse) P.lse[(int64_t)h * P.T + w.q.row0 + tk] = Ls == 0.f ? -INFINITY : (M + __log2f(Ls)) * kLn2;
+          if (P.lse) P.lse[(int64_t)h * P.T + w.q.row0 + tk] = Ls == 0.f ? -INFINITY : (M + log2f(Ls)) * kLn2;
         } else {
           float *ml = P.part_ml + ((int64_t)slot * C::BM + trow) * 2;
           ml[0] = M;

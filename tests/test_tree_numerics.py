@@ -1,7 +1,11 @@
-"""fp_tree_attn where scores jump.
+"""fp_tree_attn where its 16-bit probabilities and fp32 sums are pressed: scores that jump, V rows of very
+different sizes, values near the ends of their type, query rows of zeros.
 
-Tolerance: that of test_tree_attn.py without its share for probabilities that are small for fp16: those below
-2^-14 of the largest carry no values here.
+Tolerance: that of test_tree_attn.py, with the error of small probabilities counted token by token.  A product
+takes w = p (p times V's scale over a quantised cache) in 16 bits, and fp16 holds w to 2^-25 of the
+unit it is taken in, which is at most twice the row's largest w of the same processor when it is set; P of a tile is
+rounded again when the unit moves, up to three times: 2^-22 for each visible token.  Tokens that are not visible
+do not enter.
 """
 import math
 
@@ -79,14 +83,28 @@ def tight(c):
             P = e / e.sum(1, keepdim=True).clamp(min=1e-300)
             A = P @ vh.abs()
             dS = ((c.d + 8) * 2.0 ** -23 * size + 2.0 ** -20)[:, None]
+            if c.kind == "bf16":
+                small = 0.0
+            elif c.kind == "f16":
+                small = 2.0 ** -22 * P.amax(1, keepdim=True) * (vis.double() @ vh.abs())
+            else:
+                small = 2.0 ** -22 * vis.sum(1, keepdim=True) * (P * vh.abs().amax(1)).amax(1, keepdim=True)
             out[h, at:at + n] = P @ vh
-            bound[h, at:at + n] = (up + 2 * dS + (L / 16 + 400) * 2.0 ** -23) * A
+            bound[h, at:at + n] = (up + 2 * dS + (L / 16 + 400) * 2.0 ** -23) * A + small
             lse[h, at:at + n] = torch.where(some, torch.logsumexp(z, 1), torch.full_like(top[:, 0], -math.inf))
             lb[h, at:at + n] = dS[:, 0] + (L / 16 + 400) * 2.0 ** -23
     u = torch.finfo(c.dtype).eps / 2
     tiny = 2.0 ** -25 if c.dtype == torch.float16 else 2.0 ** -134
     bound = bound * (1 + u) + u * out.abs() + tiny
+    bound[out.abs() + bound >= torch.finfo(c.dtype).max] = math.inf  # a result that the type does not hold is infinite
     return out, bound, lse, lb + 2.0 ** -22 * lse.abs().nan_to_num(0, 0, 0)
+
+
+def normal(seed, size=1.0):
+    def make(s, n, Hkv, d):
+        g = torch.Generator("cuda").manual_seed(seed + s)
+        return size * torch.randn(n, Hkv, d, generator=g, device="cuda")
+    return make
 
 
 @pytest.mark.parametrize("kind,dtype", KINDS)
@@ -104,3 +122,38 @@ def test_scores_that_jump_after_a_plateau(fp, kind, dtype, n, g, jump):
         v[(x[:m] == 13.875).cuda()] = 1.0
         return v
     Pressed(kind, dtype, n, g, [x.tolist(), x[:128 + n].tolist()], values).check(fp)
+
+
+@pytest.mark.parametrize("kind,dtype", [("int8", "bf16"), ("e4m3", "bf16"), ("e4m3", "f16")])
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("size", [12, 22, 24, 30])
+def test_hidden_values_of_any_size_have_no_effect(fp, kind, dtype, n, g, size):
+    """A drafted token that only itself sees, its V row 2^size times the others': the other rows give what they give
+    without it, and its own is right too."""
+    masks = [[(1 << i) | (0 if i == 2 else 1) for i in range(n)]] * 2
+    res = []
+    for big in (0, size):
+        c = Case(kind, dtype, 128, 16, 2, g, [70 + n, n], [n, n], masked=True, masks=masks, seed=31)
+        for s in range(2):
+            pos = c.lens[s] - n + 2
+            c.scale[1][int(c.table[s][pos // 16]), :, pos % 16] *= 2.0 ** big
+        c.reference = lambda c=c: tight(c)
+        res.append(c.check(fp))
+    other = [i for i in range(2 * n) if i % n != 2]
+    assert torch.equal(res[0][0][:, other], res[1][0][:, other]) and torch.equal(res[0][1][:, other], res[1][1][:, other])
+
+
+@pytest.mark.parametrize("kind,dtype", KINDS)
+@pytest.mark.parametrize("n,g", ROWS)
+def test_large_values_of_tokens_without_weight(fp, kind, dtype, n, g):
+    """Small V rows carry the weight; beside them V rows 2^24 times as large (2^8 in fp16, which has no more) whose
+    probability is 2^-100."""
+    x = torch.zeros(300 + n)
+    x[5::7] = -100.0
+    far = 2.0 ** (8 if kind == "f16" else 24)
+
+    def values(s, m, Hkv, d):
+        v = 2.0 ** -6 * normal(41)(s, m, Hkv, d)
+        v[5:300:7] *= far
+        return v
+    Pressed(kind, dtype, n, g, [x.tolist()], values, gains=(1.0,)).check(fp)
