@@ -48,8 +48,9 @@
 // far apart (tree_top).
 //
 // Rounding: the products take P (times V's scale) in 16 bits, bf16 over bf16 caches and
-// fp16 elsewhere, off by at most 2^-8 or 2^-11 of each probability: as much again as
-// out's own rounding has.  With many tokens these errors average out; where one token
+// fp16 elsewhere, off by at most 2^-8 or 2^-11 of each: as much again as
+// out's own rounding has.  fp16 has that down to 2^-17 of the row's largest (of the same
+// processor), and an absolute 2^-28 of that largest below it (kLift).  With many tokens these errors average out; where one token
 // dominates a row they are common to its columns.  The sums are of the unrounded
 // values: sums of the rounded ones would make a dominated row exact, but they would bring
 // P's rounding into lse and double the bound of the others.
@@ -366,8 +367,12 @@ __device__ __forceinline__ float tree_pow2(float d) { return d < -126.f ? 0.f : 
 // What a row's weights are taken in (see Units above).
 template <int KIND>
 struct TreeUnit {
-  static constexpr float kLift = 0.f;
-  static constexpr float kSlack = KIND == kKvBf16 ? 40.f : 14.f;  // fp16 holds up to 2^15.99
+  // fp16: up to 2^15 of its 2^15.99, and the largest weight above 2^3 when the unit is set, so that
+  // 2^-17 of it is still a normal number and 2^-28 of it half of the last step.  A unit that moves
+  // costs time, mostly above 32 rows: 64 drafted tokens over 128K in e4m3 take 228 us with 0 + 14,
+  // 243 with 4 + 11, 253 with 9 + 6.
+  static constexpr float kLift = KIND == kKvBf16 ? 0.f : 4.f;
+  static constexpr float kSlack = KIND == kKvBf16 ? 40.f : 11.f;
   static constexpr float kFar = 70.f;  // 2^(s - m) stays below about 2^kFar over V rows of next to nothing
   // the unit of a row whose largest product is 2^key and whose largest score is top
   static __device__ __forceinline__ float at(float key, float top) { return ceilf(fmaxf(key, top - kFar)) - kLift; }

@@ -162,7 +162,9 @@ size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d);
  *   out[h][i] = sum_p softmax_p(scale q_i . k_p) v_p,
  *   lse[h][i] = ln sum_p exp(scale q_i . k_p)     (lse may be NULL)
  * with fp32 scores, sums and accumulation, and probabilities rounded to the
- * 16-bit type of the matrix product.  A token that sees nothing gets out 0 and
+ * 16-bit type of the matrix product: to bf16 over bf16 caches (off by at most
+ * 2^-8 of each), elsewhere to fp16, over int8 and e4m3 times V's scale (2^-11
+ * of each or 2^-26 of the row's largest, whichever is larger).  A token that sees nothing gets out 0 and
  * lse -inf.  Values that are not visible have no effect, NaN and infinities
  * included.
  *   q, out       [Hq][T][d] with strides, dtype FP_DT_BF16 or FP_DT_F16; over a

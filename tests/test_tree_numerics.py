@@ -3,9 +3,9 @@ different sizes, values near the ends of their type, query rows of zeros.
 
 Tolerance: that of test_tree_attn.py, with the error of small probabilities counted token by token.  A product
 takes w = p (p times V's scale over a quantised cache) in 16 bits, and fp16 holds w to 2^-25 of the
-unit it is taken in, which is at most twice the row's largest w of the same processor when it is set; P of a tile is
-rounded again when the unit moves, up to three times: 2^-22 for each visible token.  Tokens that are not visible
-do not enter.
+unit it is taken in, which is set so that the row's largest w of the same processor is above 2^3: 2^-28 of that largest w.
+P of a tile is rounded again when the unit moves, up to three times: 2^-26 for each visible token.  Tokens that are
+not visible do not enter.
 """
 import math
 
@@ -86,9 +86,9 @@ def tight(c):
             if c.kind == "bf16":
                 small = 0.0
             elif c.kind == "f16":
-                small = 2.0 ** -22 * P.amax(1, keepdim=True) * (vis.double() @ vh.abs())
+                small = 2.0 ** -26 * P.amax(1, keepdim=True) * (vis.double() @ vh.abs())
             else:
-                small = 2.0 ** -22 * vis.sum(1, keepdim=True) * (P * vh.abs().amax(1)).amax(1, keepdim=True)
+                small = 2.0 ** -26 * vis.sum(1, keepdim=True) * (P * vh.abs().amax(1)).amax(1, keepdim=True)
             out[h, at:at + n] = P @ vh
             bound[h, at:at + n] = (up + 2 * dS + (L / 16 + 400) * 2.0 ** -23) * A + small
             lse[h, at:at + n] = torch.where(some, torch.logsumexp(z, 1), torch.full_like(top[:, 0], -math.inf))
@@ -109,7 +109,7 @@ def normal(seed, size=1.0):
 
 @pytest.mark.parametrize("kind,dtype", KINDS)
 @pytest.mark.parametrize("n,g", ROWS)
-@pytest.mark.parametrize("jump", [24.25, 26.0])
+@pytest.mark.parametrize("jump", [24.25, 26.0, 31.5, 38.0])
 def test_scores_that_jump_after_a_plateau(fp, kind, dtype, n, g, jump):
     """Every 128 tokens: 32 low scores, 64 on a plateau of 13.875 (log2), then one far above it.  Only the plateau has values."""
     x = torch.zeros(512 + n)
@@ -157,3 +157,31 @@ def test_large_values_of_tokens_without_weight(fp, kind, dtype, n, g):
         v[5:300:7] *= far
         return v
     Pressed(kind, dtype, n, g, [x.tolist()], values, gains=(1.0,)).check(fp)
+
+
+@pytest.mark.parametrize("kind,dtype", KINDS)
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("above", [18.25, 23.5])
+def test_many_small_probabilities_beside_a_large_one(fp, kind, dtype, n, g, above):
+    """Every eighth token takes nearly all of the weight and has no values: the others' probabilities are far below
+    fp16's smallest normal number, and all of the result."""
+    x = torch.zeros(2000 + n)
+    x[::8] = above
+
+    def values(s, m, Hkv, d):
+        v = 1 + normal(51)(s, m, Hkv, d).abs()
+        v[::8] = 0
+        return 256 * v
+    Pressed(kind, dtype, n, g, [x.tolist()], values, gains=(1.0, 0.875)).check(fp)
+
+
+@pytest.mark.parametrize("kind,dtype", KINDS)
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("size", [1.0, 30.0])
+def test_long_caches_counted_token_by_token(fp, kind, dtype, n, g, size):
+    """Ordinary and far-apart scores over a cache that all processors share, V scales over many binades."""
+    c = Case(kind, dtype, 128, 64, 1, g, [20011, 300], [n, n - 1], masked=True, seed=81, size=size)
+    if kind in CODES:
+        c.scale[1].mul_(torch.exp2(torch.randint(-20, 7, c.scale[1].shape, device="cuda").float()))
+    c.reference = lambda: tight(c)
+    c.check(fp)
