@@ -371,8 +371,10 @@ struct TreeUnit {
   // 2^-17 of it is still a normal number and 2^-28 of it half of the last step.  A unit that moves
   // costs time, mostly above 32 rows: 64 drafted tokens over 128K in e4m3 take 228 us with 0 + 14,
   // 243 with 4 + 11, 253 with 9 + 6.
-  static constexpr float kLift = KIND == kKvBf16 ? 0.f : 4.f;
-  static constexpr float kSlack = KIND == kKvBf16 ? 40.f : 11.f;
+  // bf16: up to 2^-24, so that sums over 2^24 tokens do not overflow whatever V is, and 2^-86 of the
+  // largest weight is still a normal number; s - m near 40 is off by 2^-19, far below bf16's steps.
+  static constexpr float kLift = KIND == kKvBf16 ? -40.f : 4.f;
+  static constexpr float kSlack = KIND == kKvBf16 ? 16.f : 11.f;
   static constexpr float kFar = 70.f;  // 2^(s - m) stays below about 2^kFar over V rows of next to nothing
   // the unit of a row whose largest product is 2^key and whose largest score is top
   static __device__ __forceinline__ float at(float key, float top) { return ceilf(fmaxf(key, top - kFar)) - kLift; }

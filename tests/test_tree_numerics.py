@@ -175,6 +175,24 @@ def test_many_small_probabilities_beside_a_large_one(fp, kind, dtype, n, g, abov
     Pressed(kind, dtype, n, g, [x.tolist()], values, gains=(1.0, 0.875)).check(fp)
 
 
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_largest_bf16_values(fp, n, g, d):
+    """V rows of up to 2^126 while the scores rise by 39 (log2) from tile to tile and within them: results that the type holds."""
+    scores = []
+    for s in range(40):
+        x = torch.zeros(300 + n)
+        x[40:] = 30.0
+        x[100:] = 38.5
+        x[200:] = 76.0
+        scores.append(x.tolist())
+
+    def values(s, m, Hkv, d):
+        return 2.0 ** 126 * normal(61)(s, m, Hkv, d).clamp(-1, 1)
+    c = Pressed("bf16", "bf16", n, g, scores, values, d=d, Hkv=8, gains=(1.0, 0.5, 0.25))
+    c.check(fp)
+
+
 @pytest.mark.parametrize("kind,dtype", KINDS)
 @pytest.mark.parametrize("n,g", ROWS)
 @pytest.mark.parametrize("size", [1.0, 30.0])
