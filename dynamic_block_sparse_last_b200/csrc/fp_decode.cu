@@ -539,7 +539,7 @@ int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, 
   P.page = kv->g.page;
   P.page_shift = kv->g.page_shift;
   P.q_f16 = dtype == FP_DT_F16;
-  P.scale2 = scale * 1.4426950408889634f;
+  P.scale2 = std::fmin(scale * 1.4426950408889634f, 3.4028235e38f);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (kv->dtype) {
     case FP_DT_BF16: return launch_tree_kind<kKvBf16>(kv, P, bm, ctas, st);

@@ -386,6 +386,12 @@ struct TreeUnit {
 __device__ __forceinline__ float tree_top(float m, float l) {
   return l == 0.f ? -INFINITY : m + (float)((int)((__float_as_uint(l) >> 23) & 0xffu) - 127);
 }
+// What a row's products are multiplied by, above 0 and finite whatever the softmax scale and the
+// row's own power of two are, so that a hidden score stays -inf and a row of zeros (its power is
+// 2^-126) scores 0.
+__device__ __forceinline__ float tree_row_scale(float power, float scale2) {
+  return fminf(fmaxf(power * scale2, 1.1754944e-38f), 3.4028235e38f);
+}
 // log2 of a V scale; -inf for one that sets no unit (0, or not finite).
 __device__ __forceinline__ float tree_log2(float v) { return v > 0.f && v < INFINITY ? __log2f(v) : -INFINITY; }
 
@@ -604,7 +610,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
         const uint32_t dst = qbase + (((r >> 4) * C::kSteps + step) * 32 + dl) * 16 + ((r >> 3) & 1) * 4;
         asm volatile("st.shared.b32 [%0], %1;\n\tst.shared.b32 [%0+8], %2;" ::"r"(dst), "r"(lo), "r"(hi) : "memory");
       }
-      if (lane == 0) row_scale[r] = fac * P.scale2;
+      if (lane == 0) row_scale[r] = tree_row_scale(fac, P.scale2);
     }
     named_sync(1, NC);
     uint32_t qf[C::kQReg ? C::kSteps : 1][4];

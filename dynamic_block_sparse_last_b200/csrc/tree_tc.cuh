@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (C::kQuant && !P.q_f16) fac = tc_q_f16<LR>(x[i]);
           const uint32_t dst = sq + (PAIR ? t * C::kOp : 0) + tc_off(r, lane % LR);
           sts128(dst, x[i].x, x[i].y, x[i].z, x[i].w);
-          if (lane % LR == 0) row_scale[PAIR ? t : 0][r] = fac * P.scale2;
+          if (lane % LR == 0) row_scale[PAIR ? t : 0][r] = tree_row_scale(fac, P.scale2);
         }
         fence_async_shared();
       }

@@ -193,6 +193,18 @@ def test_largest_bf16_values(fp, n, g, d):
     c.check(fp)
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("scale", [2.0 ** -30, 2.0 ** -100, 3e38])
+def test_query_rows_of_zeros_and_scales_of_any_size(fp, kind, n, g, scale):
+    """Rows of zeros see their tokens alike, whatever the scale is; masks hide some."""
+    c = Case(kind, "bf16", 128, 16, 1, g, [90 + n, n], [n, n], masked=True, seed=71)
+    c.q = torch.zeros_like(c.q)
+    c.k_scale = scale
+    c.reference = lambda: tight(c)
+    c.check(fp)
+
+
 @pytest.mark.parametrize("kind,dtype", KINDS)
 @pytest.mark.parametrize("n,g", ROWS)
 @pytest.mark.parametrize("size", [1.0, 30.0])
