@@ -12,7 +12,7 @@ ROOT = os.path.dirname(PKG)
 SRCS = [os.path.join(PKG, "csrc", f) for f in ("fp_sparse.cu", "fp_decode.cu", "fp_prefill.cpp")]
 DEPS = SRCS + [os.path.join(PKG, "csrc", f) for f in ("ptx.cuh", "index_kernels.cuh", "attn_kernel.cuh",
                                                       "rope_pool.cuh", "share_kernels.cuh", "fp_internal.h",
-                                                      "rope_kernel.cuh", "kv_kernels.cuh", "tree_kernels.cuh", "tree_tc.cuh")] \
+                                                      "decode_sizes.h", "rope_kernel.cuh", "kv_kernels.cuh", "tree_kernels.cuh", "tree_tc.cuh")] \
     + [os.path.join(ROOT, "include", f) for f in ("fp_sparse.h", "fp_prefill.h", "fp_decode.h")]
 LIB = os.path.join(PKG, "_lib", "libfpsparse.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")

@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <new>
 
+#include "decode_sizes.h"
 #include "fp_decode.h"
 #include "fp_internal.h"
 #include "kv_kernels.cuh"
@@ -383,30 +384,13 @@ int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const
 // ---------------------------------------------------------------------------
 namespace {
 
-size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
-
 bool tree_shape_ok(int nseq, int max_q, int Hq, int Hkv, int d) {
   return nseq >= 0 && max_q >= 1 && max_q <= 256 && Hkv > 0 && Hq > 0 && Hq % Hkv == 0 && Hq / Hkv <= 256 &&
          (d == 64 || d == 128);
 }
 
-// Query rows of a unit for at most `rows` rows of a KV head, and the CTAs that go
-// with it.
-int tree_bm(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : 256; }
 constexpr int kTreeLeastBN = 64;  // the shortest of all kernels' token tiles
-int tree_ctas(int bm, int d) { return bm == 16 || (bm == 32 && d == 64) ? 2 * sms() : sms(); }
-
-struct TreeWork {
-  size_t part, ml, desc, bytes;
-};
-TreeWork tree_work(int ctas, int bm, int d) {
-  TreeWork w;
-  w.part = 0;
-  w.ml = round_up((size_t)2 * ctas * bm * d * 4);
-  w.desc = w.ml + round_up((size_t)2 * ctas * bm * 8);
-  w.bytes = w.desc + round_up((size_t)ctas * sizeof(TreeDesc));
-  return w;
-}
+static_assert(sizeof(TreeDesc) == kTreeDescBytes, "the workspace's descriptors");
 
 // Raises a kernel's shared-memory limit, once in a context; `where` is the kernel's
 // own record of the contexts it was raised in, by device.
@@ -478,8 +462,7 @@ extern "C" {
 size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d) {
   if (!tree_shape_ok(nseq, max_q, Hq, Hkv, d)) return 0;
   if (!sms()) return 0;
-  const int bm = tree_bm(max_q * (Hq / Hkv));
-  return tree_work(tree_ctas(bm, d), bm, d).bytes;
+  return tree_workspace(max_q * (Hq / Hkv), d, sms());
 }
 
 int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, int dtype, int T, int Hq,
@@ -500,7 +483,7 @@ int fp_tree_attn(const fp_kv *kv, const void *q, int64_t q_tok, int64_t q_head, 
   if (!on_device(kv)) return FP_ERR_ARG;
   if (!sms()) return FP_ERR_CUDA;
   const int g = Hq / kv->g.heads, bm = tree_bm(max_q * g);
-  const int most = tree_ctas(bm, kv->d);
+  const int most = tree_ctas(bm, kv->d, sms());
   const TreeWork w = tree_work(most, bm, kv->d);
   if (work_bytes < w.bytes) return FP_ERR_ARG;
   // no more CTAs than there can be tiles

@@ -148,7 +148,7 @@ int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const
 
 /* Bytes of device workspace that fp_tree_attn needs for these sizes on the
  * current device (0 for sizes that it does not take): nseq sequences of at most
- * max_q new tokens.  The contents need not be set, and are not kept between
+ * max_q new tokens; it also serves calls with a smaller max_q or fewer query heads.  The contents need not be set, and are not kept between
  * calls; calls that may run at the same time, captured graphs among them, need
  * a workspace each. */
 size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d);

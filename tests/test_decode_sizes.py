@@ -1,0 +1,37 @@
+"""Grids and workspaces of the serving calls (csrc/decode_sizes.h), compiled for the host."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "dynamic_block_sparse_last_b200", "csrc")
+
+SHIM = """
+#include "decode_sizes.h"
+extern "C" size_t need(int rows, int d, int sms) {      // what a call of exactly these rows checks for
+  const int bm = fpk::tree_bm(rows);
+  return fpk::tree_work(fpk::tree_ctas(bm, d, sms), bm, d).bytes;
+}
+extern "C" size_t space(int rows, int d, int sms) { return fpk::tree_workspace(rows, d, sms); }
+"""
+
+
+@pytest.fixture(scope="module")
+def sizes(tmp_path_factory):
+    at = tmp_path_factory.mktemp("sizes")
+    (at / "shim.cpp").write_text(SHIM)
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", "-I" + CSRC, str(at / "shim.cpp"),
+                           "-o", str(at / "shim.so")])
+    lib = ctypes.CDLL(str(at / "shim.so"))
+    lib.need.restype = lib.space.restype = ctypes.c_size_t
+    return lib
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("sms", [1, 7, 132, 148, 160])
+def test_a_workspace_serves_every_call_with_fewer_rows(sizes, d, sms):
+    most = 0
+    for rows in [*range(1, 300), 1000, 65536]:
+        most = max(most, sizes.need(rows, d, sms))
+        assert sizes.space(rows, d, sms) == most

@@ -215,3 +215,16 @@ def test_long_caches_counted_token_by_token(fp, kind, dtype, n, g, size):
         c.scale[1].mul_(torch.exp2(torch.randint(-20, 7, c.scale[1].shape, device="cuda").float()))
     c.reference = lambda: tight(c)
     c.check(fp)
+
+
+def test_a_workspace_for_the_longest_drafts_serves_shorter_ones(fp):
+    for d in (64, 128):
+        for g in (1, 3, 4, 16, 40, 256):
+            size = 0
+            for max_q in (1, 2, 4, 5, 8, 9, 16, 33, 64, 65, 256):
+                now = fp.fp_tree_attn_workspace(3, max_q, 2 * g, 2, d)
+                assert now >= size, (d, g, max_q)
+                size = now
+    c = Case("int8", "bf16", 128, 16, 2, 4, [300, 77], [1, 1], seed=91, max_q=1)
+    work = torch.empty(fp.fp_tree_attn_workspace(2, 8, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    c.check(fp, work=work)
