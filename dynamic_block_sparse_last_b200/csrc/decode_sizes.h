@@ -3,10 +3,35 @@
 #pragma once
 
 #include <stddef.h>
+#include <stdint.h>
 
 #include <initializer_list>
 
 namespace fpk {
+
+// Tokens and heads of a block of fp_kv_write and fp_kv_read: 32 tokens of all heads, so
+// that the slots are looked up once for them, while that makes about eight blocks per
+// multiprocessor (enough to fill it); with less work, fewer heads, and then 16 tokens.
+struct KvSplit {
+  int shift, group;          // log2 of the tokens, heads
+  unsigned blocks, groups;   // the grid
+};
+inline KvSplit kv_split(int heads, int T, int sms) {
+  KvSplit s;
+  const int64_t want = 8 * (int64_t)(sms > 0 ? sms : 1);
+  s.shift = 5;
+  int64_t blocks = ((int64_t)T + 31) / 32;
+  if (blocks * heads < want) {
+    s.shift = 4;
+    blocks = ((int64_t)T + 15) / 16;
+  }
+  int64_t groups = (want + blocks - 1) / blocks;
+  if (groups > heads) groups = heads;
+  s.group = (int)((heads + groups - 1) / groups);
+  s.blocks = (unsigned)blocks;
+  s.groups = (unsigned)((heads + s.group - 1) / s.group);
+  return s;
+}
 
 inline size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 

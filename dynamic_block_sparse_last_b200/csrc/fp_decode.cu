@@ -214,29 +214,6 @@ bool on_device(const fp_kv *kv) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
 }
 
-// Tokens and heads of a block: 32 tokens of all heads, so that the slots are looked
-// up once for them, while that makes about eight blocks per multiprocessor (enough to
-// fill it); with less work, fewer heads, and then 16 tokens.
-struct KvSplit {
-  int shift, group;
-  dim3 grid;
-};
-KvSplit kv_split(int heads, int T) {
-  KvSplit s;
-  const int64_t want = 8 * (int64_t)sms();
-  s.shift = 5;
-  int64_t blocks = (T + 31) / 32;
-  if (blocks * heads < want) {
-    s.shift = 4;
-    blocks = (T + 15) / 16;
-  }
-  int64_t groups = (want + blocks - 1) / blocks;
-  if (groups > heads) groups = heads;
-  s.group = (int)((heads + groups - 1) / groups);
-  s.grid = dim3((unsigned)blocks, (unsigned)((heads + s.group - 1) / s.group));
-  return s;
-}
-
 template <int KIND, typename T>
 int launch_kv_write(const KvWriteParams &P, int d, dim3 grid, cudaStream_t st) {
   if (d == 128) k_kv_write<KIND, T, 128><<<grid, kKvThreads, 0, st>>>(P);
@@ -324,6 +301,7 @@ int fp_kv_write(const fp_kv *kv, const void *k, int64_t k_tok, int64_t k_head, c
   if (v && !rows_ok(v, v_tok, v_head, size)) return FP_ERR_ARG;
   if (!slots || !multiple_of(slots, 8)) return FP_ERR_ARG;
   if (!on_device(kv)) return FP_ERR_ARG;
+  if (!sms()) return FP_ERR_CUDA;
   KvWriteParams P;
   P.g = kv->g;
   P.in[0] = k;
@@ -334,12 +312,12 @@ int fp_kv_write(const fp_kv *kv, const void *k, int64_t k_tok, int64_t k_head, c
   P.head[1] = v_head;
   P.slots = slots;
   P.T = T;
-  const KvSplit split = kv_split(kv->g.heads, T);
+  const KvSplit split = kv_split(kv->g.heads, T, sms());
   P.group = split.group;
   P.tok_shift = split.shift;
   P.err = library_error_word();
   if (!P.err) return FP_ERR_CUDA;
-  return launch_kv(kv->dtype, dtype, P, kv->d, split.grid, static_cast<cudaStream_t>(stream));
+  return launch_kv(kv->dtype, dtype, P, kv->d, dim3(split.blocks, split.groups), static_cast<cudaStream_t>(stream));
 }
 
 int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const int32_t *cu, const int32_t *first,
@@ -355,6 +333,7 @@ int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const
   if (!block_table || !cu || !multiple_of(block_table, 4) || !multiple_of(cu, 4) || !multiple_of(first, 4))
     return FP_ERR_ARG;
   if (!on_device(kv)) return FP_ERR_ARG;
+  if (!sms()) return FP_ERR_CUDA;
   KvReadParams P;
   P.g = kv->g;
   P.out[0] = k;
@@ -369,12 +348,12 @@ int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const
   P.max_pages = max_pages;
   P.nseq = nseq;
   P.T = T;
-  const KvSplit split = kv_split(kv->g.heads, T);
+  const KvSplit split = kv_split(kv->g.heads, T, sms());
   P.group = split.group;
   P.tok_shift = split.shift;
   P.err = library_error_word();
   if (!P.err) return FP_ERR_CUDA;
-  return launch_kv(kv->dtype, dtype, P, kv->d, split.grid, static_cast<cudaStream_t>(stream));
+  return launch_kv(kv->dtype, dtype, P, kv->d, dim3(split.blocks, split.groups), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
