@@ -392,6 +392,12 @@ __device__ __forceinline__ float tree_top(float m, float l) {
 __device__ __forceinline__ float tree_row_scale(float power, float scale2) {
   return fminf(fmaxf(power * scale2, 1.1754944e-38f), 3.4028235e38f);
 }
+// The power of two by which a bf16 query row of largest magnitude mx is divided for fp16, which
+// leaves it below 4; 0 for a row that is not finite.
+__device__ __forceinline__ int tree_q_exp(float mx) {
+  const int e = (int)(__float_as_uint(mx) >> 23) - 127;  // mx in [2^e, 2^(e+1))
+  return e > 127 ? 0 : min(max(e, -126), 126);
+}
 // log2 of a V scale; -inf for one that sets no unit (0, or not finite).
 __device__ __forceinline__ float tree_log2(float v) { return v > 0.f && v < INFINITY ? __log2f(v) : -INFINITY; }
 
@@ -597,8 +603,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
                       __uint_as_float(hi & 0xffff0000u)};
         float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
         mx = redux_max_f32(mx);
-        int e = (int)(__float_as_uint(mx) >> 23) - 127;  // largest in [2^e, 2^(e+1))
-        e = e > 126 ? 0 : (e < -126 ? -126 : e);
+        const int e = tree_q_exp(mx);
         fac = pow2i(e);
         const float inv = pow2i(-e);
         lo = pack_f16x2(x[0] * inv, x[1] * inv);

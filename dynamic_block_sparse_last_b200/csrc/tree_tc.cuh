@@ -176,8 +176,7 @@ __device__ __forceinline__ float tc_q_f16(uint4 &x) {
   for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(f[e]));
 #pragma unroll
   for (int o = LR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  int e = (int)(__float_as_uint(mx) >> 23) - 127;  // largest in [2^e, 2^(e+1))
-  e = e > 126 ? 0 : (e < -126 ? -126 : e);
+  const int e = tree_q_exp(mx);
   const float inv = pow2i(-e);
   x = make_uint4(pack_f16x2(f[0] * inv, f[1] * inv), pack_f16x2(f[2] * inv, f[3] * inv), pack_f16x2(f[4] * inv, f[5] * inv),
                  pack_f16x2(f[6] * inv, f[7] * inv));

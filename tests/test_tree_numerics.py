@@ -20,6 +20,7 @@ pytestmark = pytest.mark.gpu
 ROWS = [(4, 2), (12, 2), (32, 2), (64, 4)]
 
 
+
 class Pressed(Case):
     """A case whose scores and values are given: every query row is its gain times the first unit vector, a cached key the
     score (in log2 units) times it."""
@@ -228,3 +229,15 @@ def test_a_workspace_for_the_longest_drafts_serves_shorter_ones(fp):
     c = Case("int8", "bf16", 128, 16, 2, 4, [300, 77], [1, 1], seed=91, max_q=1)
     work = torch.empty(fp.fp_tree_attn_workspace(2, 8, 8, 2, 128), dtype=torch.uint8, device="cuda")
     c.check(fp, work=work)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,g", ROWS)
+def test_largest_bf16_queries(fp, kind, n, g):
+    """Query rows whose largest element is 2^127 or more, under a softmax scale that brings their scores back."""
+    c = Case(kind, "bf16", 128, 16, 1, g, [90 + n, n], [n, n], masked=True, seed=101)
+    c.q = (c.q.double() * 2.0 ** 125).clamp(-3.3e38, 3.3e38).to(torch.bfloat16)
+    assert bool((c.q.float().abs().amax(-1) >= 2.0 ** 127).any())
+    c.k_scale *= 2.0 ** -125
+    c.reference = lambda: tight(c)
+    c.check(fp)
