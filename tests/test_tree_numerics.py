@@ -20,7 +20,6 @@ pytestmark = pytest.mark.gpu
 ROWS = [(4, 2), (12, 2), (32, 2), (64, 4)]
 
 
-
 class Pressed(Case):
     """A case whose scores and values are given: every query row is its gain times the first unit vector, a cached key the
     score (in log2 units) times it."""
@@ -110,17 +109,21 @@ def normal(seed, size=1.0):
 
 @pytest.mark.parametrize("kind,dtype", KINDS)
 @pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("plateau", [10.875, 13.875])
 @pytest.mark.parametrize("jump", [24.25, 26.0, 31.5, 38.0])
-def test_scores_that_jump_after_a_plateau(fp, kind, dtype, n, g, jump):
-    """Every 128 tokens: 32 low scores, 64 on a plateau of 13.875 (log2), then one far above it.  Only the plateau has values."""
+def test_scores_that_jump_after_a_plateau(fp, kind, dtype, n, g, jump, plateau):
+    """Every 128 tokens: 32 low scores, 64 on a plateau (log2), then one far above it.  Only the plateau has values
+    in all columns but the last, where the others have theirs, so that the rows are alike in size."""
     x = torch.zeros(512 + n)
     for a in range(0, 512, 128):
-        x[a + 32:a + 96] = 13.875
+        x[a + 32:a + 96] = plateau
         x[a + 96 + a // 16] = jump
 
     def values(s, m, Hkv, d):
         v = torch.zeros(m, Hkv, d, device="cuda")
-        v[(x[:m] == 13.875).cuda()] = 1.0
+        on = (x[:m] == plateau).cuda()
+        v[on, :, :-1] = 1.0
+        v[~on, :, -1] = 1.0
         return v
     Pressed(kind, dtype, n, g, [x.tolist(), x[:128 + n].tolist()], values).check(fp)
 
