@@ -294,8 +294,8 @@ int fp_kv_write(const fp_kv *kv, const void *k, int64_t k_tok, int64_t k_head, c
                 int64_t v_head, int dtype, int T, const int64_t *slots, void *stream) {
   if (!kv || T < 0) return FP_ERR_ARG;
   if (dtype != FP_DT_BF16 && dtype != FP_DT_F16 && dtype != FP_DT_F32) return FP_ERR_ARG;
-  if (!k && !v) return FP_ERR_ARG;
   if (T == 0) return FP_OK;
+  if (!k && !v) return FP_ERR_ARG;
   const int size = size_of(dtype);
   if (k && !rows_ok(k, k_tok, k_head, size)) return FP_ERR_ARG;
   if (v && !rows_ok(v, v_tok, v_head, size)) return FP_ERR_ARG;
@@ -325,8 +325,8 @@ int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const
                int dtype, void *stream) {
   if (!kv || T < 0 || nseq < 0 || max_pages < 0) return FP_ERR_ARG;
   if (dtype != FP_DT_BF16 && dtype != FP_DT_F16 && dtype != FP_DT_F32) return FP_ERR_ARG;
-  if (!k && !v) return FP_ERR_ARG;
   if (T == 0 || nseq == 0) return FP_OK;
+  if (!k && !v) return FP_ERR_ARG;
   const int size = size_of(dtype);
   if (k && !rows_ok(k, k_tok, k_head, size)) return FP_ERR_ARG;
   if (v && !rows_ok(v, v_tok, v_head, size)) return FP_ERR_ARG;

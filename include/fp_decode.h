@@ -139,7 +139,7 @@ int fp_kv_write(const fp_kv *kv, const void *k, int64_t k_tok, int64_t k_head, c
  *   first        device int32[nseq] or NULL for 0 (4-byte aligned, all three)
  * T is the number of rows of the outputs; rows behind cu[nseq] are left as they
  * were, and so are rows whose position or page is out of range (FP_ERR_RANGE).
- * k or v may be NULL to read the other alone. */
+ * k or v may be NULL to read the other alone.  T = 0 or nseq = 0 is a no-op. */
 int fp_kv_read(const fp_kv *kv, const int32_t *block_table, int max_pages, const int32_t *cu, const int32_t *first,
                int nseq, int T, void *k, int64_t k_tok, int64_t k_head, void *v, int64_t v_tok, int64_t v_head,
                int dtype, void *stream);

@@ -346,3 +346,29 @@ def test_refusals_of_the_binding(fp):
     x = rand((2, 5, 64), torch.bfloat16, 9).view(-1)[4:4 + 2 * 4 * 64].view(2, 4, 64)  # rows 8 bytes off
     with pytest.raises(fp.FpError):
         kv.write(x, None, slots)
+
+
+@pytest.mark.parametrize("kind", ["int8", "bf16"])
+def test_calls_without_tokens(fp, kind):
+    """No tokens, as a step without new ones has it (empty tensors have no address): nothing happens."""
+    hkv, d = 2, 64
+    p = pools(kind, 2, hkv, 16, d)
+    before = [raw(x).clone() for x in p[:2]]
+    kv = fp.KvCache(*p)
+    k = torch.empty(hkv, 0, d, device="cuda", dtype=torch.bfloat16)
+    none = torch.empty(0, device="cuda")
+    kv.write(k, k, none.long())
+    kv.write(k, None, none.long())
+    table, cu = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.zeros(2, dtype=torch.int32, device="cuda")
+    kv.read(table, cu, k, k)
+    kv.read(table, cu, None, k)
+    kv.read(table[:0], cu[:1], rand((hkv, 3, d), torch.bfloat16, 11), None)
+    q = torch.empty(4, 0, d, device="cuda", dtype=torch.bfloat16)
+    pos = none.int()
+    fp.Rope(d).apply(q, k, q, k, pos)
+    work = torch.empty(fp.fp_tree_attn_workspace(1, 1, 4, hkv, d), dtype=torch.uint8, device="cuda")
+    fp.fp_tree_attn(q, kv, table, cu[:1], cu, 1, torch.empty(0, 1, dtype=torch.int64, device="cuda"), 0.125, torch.empty_like(q), work,
+                    lse=torch.empty(4, 0, device="cuda"))
+    torch.cuda.synchronize()
+    assert fp.fp_get_device_error() == fp.FP_OK
+    assert all(torch.equal(raw(x), y) for x, y in zip(p[:2], before))
