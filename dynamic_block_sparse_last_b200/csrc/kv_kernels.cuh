@@ -19,9 +19,9 @@
 // Bound: memory, each byte once.  A block takes some neighbouring tokens and a
 // group of heads: it looks the tokens' slots up once, into shared memory, and
 // then moves rows in 16-byte vectors, several rows in flight per thread.  Measured
-// over 8 heads of 128: 43.7 K bf16 tokens to e4m3 in 64 us (4.2 TB/s; the integer pipe
-// is 61% busy, with a division per element it took 136 us), back in 44 us (6.1 TB/s);
-// 131072 int8 tokens back in 127 us (6.4 TB/s).
+// over 8 heads of 128: 43.7 K bf16 tokens to e4m3 in 65 us (4.2 TB/s; the integer pipe
+// is 61% busy, with a division per element it took 136 us), back in 47 us (5.8 TB/s);
+// 131072 int8 tokens back in 131 us (6.2 TB/s).
 #pragma once
 
 #include <type_traits>
@@ -31,7 +31,7 @@
 
 namespace fpk {
 
-constexpr int kKvTokens = 64;    // most tokens of a block
+constexpr int kKvTokens = 32;    // most tokens of a block (kv_split)
 constexpr int kKvThreads = 256;
 
 struct KvGeom {

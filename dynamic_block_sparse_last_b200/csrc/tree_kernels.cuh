@@ -24,7 +24,7 @@
 //
 // Measured (32 query heads, 8 KV heads of 128): 64 sequences of up to 16384 tokens,
 // one new token each, over bf16 in 365 us, 6.4 TB/s (0.97 of the measured copy); over
-// int8 in 231 us, 5.2 TB/s (244 us after seconds under load, as the clock falls):
+// int8 in 235 us, 5.1 TB/s (250 to 256 us after seconds under load, as the clock falls):
 // there a warp's chain of conversion, product, softmax and product is what two warps
 // a scheduler do not hide (issue slots 49% busy).
 //
@@ -375,7 +375,9 @@ struct TreeUnit {
   // largest weight is still a normal number; s - m near 40 is off by 2^-19, far below bf16's steps.
   static constexpr float kLift = KIND == kKvBf16 ? -40.f : 4.f;
   static constexpr float kSlack = KIND == kKvBf16 ? 16.f : 11.f;
-  static constexpr float kFar = 70.f;  // 2^(s - m) stays below about 2^kFar over V rows of next to nothing
+  // Over V rows of next to nothing 2^(s - m) stays below 2^(kFar + kLift + kSlack), and its sum over 2^30
+  // tokens below 2^127; V scales from 2^-kFar on set their unit themselves.
+  static constexpr float kFar = 82.f;
   // the unit of a row whose largest product is 2^key and whose largest score is top
   static __device__ __forceinline__ float at(float key, float top) { return ceilf(fmaxf(key, top - kFar)) - kLift; }
   // log2 of the largest of some V scales, as the bound takes it
@@ -888,7 +890,7 @@ __global__ void __launch_bounds__((TreeCfg<KIND, D, MT>::kThreads), (TreeCfg<KIN
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bar_empty[st]));
     }
-    // ---- join the four warps
+    // ---- join the warps
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

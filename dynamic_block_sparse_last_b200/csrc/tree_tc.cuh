@@ -30,9 +30,10 @@
 // Sums are of the unrounded exponentials.
 //
 // Measured (32 query heads, 8 KV heads of 128): 64 drafted tokens over 131072 cached in
-// bf16 in 173 us (794 TFLOP/s), in e4m3 in 220 to 232 us; 16 drafted tokens for 8
-// sequences of up to 32768 in bf16 in 141 us, 5.4 TB/s.  Of 256 rows over 8 bits a tile
-// takes about 6200 clocks: softmax 4100, then the wait for PV and QK; the products need
+// bf16 in 172 us (799 TFLOP/s), in e4m3 in 235 to 243 us; 16 drafted tokens for 8
+// sequences of up to 32768 in bf16 in 142 us, 5.4 TB/s (157 to 160 us, 4.8 TB/s, after
+// seconds under load).  Of 256 rows over 8 bits a tile took about 6200 clocks when that took
+// 220 us (units move more often since): softmax 4100, then the wait for PV and QK; the products need
 // 2048, shared memory (Q twice, K and V twice, the conversion's traffic) about 2560.
 //
 // The K/V warps read shared memory that TMA filled and not global memory: the

@@ -544,7 +544,7 @@ class KvCache:
 
 
 def fp_tree_attn_workspace(nseq, max_q, Hq, Hkv, d) -> int:
-    """Bytes of workspace of fp_tree_attn on the current device."""
+    """Bytes of workspace of fp_tree_attn on the current device, for at most max_q new tokens a sequence."""
     n = _lib.fp_tree_attn_workspace(nseq, max_q, Hq, Hkv, d)
     if n == 0:
         _refuse("fp_tree_attn_workspace", "sizes out of range, or no usable device")

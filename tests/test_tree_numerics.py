@@ -244,3 +244,16 @@ def test_largest_bf16_queries(fp, kind, n, g):
     c.k_scale *= 2.0 ** -125
     c.reference = lambda: tight(c)
     c.check(fp)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("n,g", ROWS)
+@pytest.mark.parametrize("size", [-80, -60, 60, 80])
+def test_v_scales_at_the_ends_of_their_range(fp, kind, n, g, size):
+    """All V scales near 2^size, scores far apart: the results are those at 2^0, times 2^size."""
+    c = Case(kind, "bf16", 128, 64, 1, g, [1500 + n, 200], [n, n - 1], masked=True, seed=111, size=3.0)
+    for pool in c.scale[1:]:                     # powers of two, so that the results scale exactly
+        pool.copy_(torch.exp2(torch.log2(pool).floor()).nan_to_num(1.0))
+        pool.mul_(2.0 ** (size - math.log2(float(pool.min()))))
+    c.reference = lambda: tight(c)
+    c.check(fp)
