@@ -178,8 +178,7 @@ template <int KIND, typename T, int D>
 __global__ void __launch_bounds__(kKvThreads) k_kv_write(const KvWriteParams P) {
   constexpr int V = RopeVec<T>::kElems;      // elements of a lane
   constexpr int L = D / V;                   // lanes of a row
-  constexpr int R = kKvThreads / L;          // rows of the block at a time
-  constexpr int U = 1;                       // of them in flight a thread (2 measured the same)
+  constexpr int R = kKvThreads / L;          // rows of the block at a time (two a thread measured the same)
   __shared__ int64_t slot_sh[kKvTokens];
   const int tokens = 1 << P.tok_shift;
   const int t0 = blockIdx.x << P.tok_shift;
@@ -195,80 +194,72 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_write(const KvWriteParams P) 
   const int h0 = blockIdx.y * P.group, nh = min(P.group, P.g.heads - h0);
   const int lane = threadIdx.x % L, r0 = threadIdx.x / L;
   const int rows = tokens * nh;
-  for (int base = 0; base < rows; base += U * R) {  // whole warps take part in the row maxima
-    int64_t row[U];
-    uint4 raw[U][2];
+  for (int base = 0; base < rows; base += R) {  // whole warps take part in the row maxima
+    const int r = base + r0, tt = r & (tokens - 1), h = h0 + (r >> P.tok_shift);
+    const int64_t slot = r < rows ? slot_sh[tt] : -1;
+    const int64_t row = slot < 0 ? -1 : (((slot >> P.g.page_shift) * P.g.heads + h) << P.g.page_shift) + (slot & (P.g.page - 1));
+    uint4 raw[2];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = base + u * R + r0, tt = r & (tokens - 1), h = h0 + (r >> P.tok_shift);
-      const int64_t slot = r < rows ? slot_sh[tt] : -1;
-      row[u] = slot < 0 ? -1 : (((slot >> P.g.page_shift) * P.g.heads + h) << P.g.page_shift) + (slot & (P.g.page - 1));
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        raw[u][w] = make_uint4(0, 0, 0, 0);
-        if (slot >= 0 && P.in[w])
-          raw[u][w] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(P.in[w]) + (t0 + tt) * P.tok[w] +
-                                                       h * P.head[w] + lane * V);
-      }
+    for (int w = 0; w < 2; ++w) {
+      raw[w] = make_uint4(0, 0, 0, 0);
+      if (slot >= 0 && P.in[w])
+        raw[w] = *reinterpret_cast<const uint4 *>(static_cast<const T *>(P.in[w]) + (t0 + tt) * P.tok[w] + h * P.head[w] +
+                                                  lane * V);
     }
-    float Ms[U][2];
+    float Ms[2];
     if constexpr (KvCode<KIND>::kQuant) {
-      // the scales of the rows in flight, one division for all: lane 2 u + w makes one
+      // the two scales, one division for both: lane w makes one
       float M = 0.f;
       int64_t at = -1;
       int kv = 0;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          Ms[u][w] = kv_row_max<T, L>(raw[u][w]);
-          if (lane == 2 * u + w && P.in[w]) {
-            M = Ms[u][w];
-            at = row[u];
-            kv = w;
-          }
+      for (int w = 0; w < 2; ++w) {
+        Ms[w] = kv_row_max<T, L>(raw[w]);
+        if (lane == w && P.in[w]) {
+          M = Ms[w];
+          at = row;
+          kv = w;
         }
+      }
       if (at >= 0) P.g.scale[kv][at] = M < INFINITY ? __fdiv_rn(M, KvCode<KIND>::kTop) : __uint_as_float(0x7fc00000u);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int w = 0; w < 2; ++w) {
+      if (!P.in[w]) continue;
+      float x[V];
+      RopeVec<T>::unpack(raw[w], x);
+      if constexpr (KvCode<KIND>::kQuant) {
+        constexpr bool kExact = sizeof(T) == 4;
+        const float M = Ms[w];
+        uint32_t code[V / 4] = {};
+        if (M > 1e-30f && M < 1e30f) {
+          kv_quantise<KIND, V, kExact>(x, M, code);
+        } else if (M > 0.f && M < INFINITY) {
+          // c / M would leave fp32: the row times 2^100 or 2^-100, which the quotient does not see
+          const float f = M < 1.f ? 1.2676506002282294e30f : 7.888609052210118e-31f;
+          float z[V];
 #pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        if (!P.in[w]) continue;
-        float x[V];
-        RopeVec<T>::unpack(raw[u][w], x);
-        if constexpr (KvCode<KIND>::kQuant) {
-          constexpr bool kExact = sizeof(T) == 4;
-          const float M = Ms[u][w];
-          uint32_t code[V / 4] = {};
-          if (M > 1e-30f && M < 1e30f) {
-            kv_quantise<KIND, V, kExact>(x, M, code);
-          } else if (M > 0.f && M < INFINITY) {
-            // c / M would leave fp32: the row times 2^100 or 2^-100, which the quotient does not see
-            const float f = M < 1.f ? 1.2676506002282294e30f : 7.888609052210118e-31f;
-            float z[V];
+          for (int i = 0; i < V; ++i) z[i] = x[i] * f;
+          kv_quantise<KIND, V, kExact>(z, M * f, code);
+        }
+        if (row >= 0) {
+          uint8_t *dst = static_cast<uint8_t *>(P.g.pool[w]) + row * D + lane * V;
+          if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
+          else *reinterpret_cast<uint32_t *>(dst) = code[0];
+        }
+      } else if (row >= 0) {
+        using C = typename std::conditional<KIND == kKvBf16, __nv_bfloat16, __half>::type;
+        C *dst = static_cast<C *>(P.g.pool[w]) + row * D + lane * V;
+        if constexpr (V == 8) {
+          *reinterpret_cast<uint4 *>(dst) = RopeVec<C>::pack(x);
+        } else {
+          C y[4];
 #pragma unroll
-            for (int i = 0; i < V; ++i) z[i] = x[i] * f;
-            kv_quantise<KIND, V, kExact>(z, M * f, code);
-          }
-          if (row[u] >= 0) {
-            uint8_t *dst = static_cast<uint8_t *>(P.g.pool[w]) + row[u] * D + lane * V;
-            if constexpr (V == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
-            else *reinterpret_cast<uint32_t *>(dst) = code[0];
-          }
-        } else if (row[u] >= 0) {
-          using C = typename std::conditional<KIND == kKvBf16, __nv_bfloat16, __half>::type;
-          C *dst = static_cast<C *>(P.g.pool[w]) + row[u] * D + lane * V;
-          if constexpr (V == 8) {
-            *reinterpret_cast<uint4 *>(dst) = RopeVec<C>::pack(x);
-          } else {
-            C y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = rope_from_float<C>(x[i]);
-            *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(y);
-          }
+          for (int i = 0; i < 4; ++i) y[i] = rope_from_float<C>(x[i]);
+          *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(y);
         }
       }
+    }
   }
 }
 
