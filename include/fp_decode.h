@@ -165,7 +165,8 @@ size_t fp_tree_attn_workspace(int nseq, int max_q, int Hq, int Hkv, int d);
  * 16-bit type of the matrix product: to bf16 over bf16 caches (off by at most
  * 2^-8 of each), elsewhere to fp16, over int8 and e4m3 times V's scale (2^-11
  * of each or 2^-26 of the row's largest, whichever is larger; V's scales
- * from 2^-80 to 2^80).  A token that sees nothing gets out 0 and
+ * from 2^-80 to 2^80).  Probabilities below 2^-80 of the row's largest may count
+ * as 0.  A token that sees nothing gets out 0 and
  * lse -inf.  Values that are not visible have no effect, NaN and infinities
  * included.
  *   q, out       [Hq][T][d] with strides, dtype FP_DT_BF16 or FP_DT_F16; over a

@@ -257,3 +257,17 @@ def test_v_scales_at_the_ends_of_their_range(fp, kind, n, g, size):
         pool.mul_(2.0 ** (size - math.log2(float(pool.min()))))
     c.reference = lambda: tight(c)
     c.check(fp)
+
+
+@pytest.mark.parametrize("kind,dtype", [("bf16", "bf16"), ("int8", "bf16"), ("e4m3", "bf16")])
+@pytest.mark.parametrize("n,g", ROWS)
+def test_tokens_far_below_one_that_holds_zeros(fp, kind, dtype, n, g):
+    """All of a result from probabilities of 2^-60, the likely tokens' V rows being zeros."""
+    x = torch.zeros(700 + n)
+    x[::9] = 60.0
+
+    def values(s, m, Hkv, d):
+        v = normal(121)(s, m, Hkv, d)
+        v[::9] = 0
+        return v
+    Pressed(kind, dtype, n, g, [x.tolist()], values, gains=(1.0, 0.5)).check(fp)
